@@ -11,12 +11,16 @@
 #include <atomic>
 #include <mutex>
 
+#include "api_checks.h"
 #include "hts.h"
 #include "hts_internal.h"
 
-namespace {
+namespace hts {
+namespace api {
 
+namespace {
 thread_local char g_err[512];
+}
 
 hts_status fail(hts_status s, const char* fmt, ...) {
     va_list ap;
@@ -31,30 +35,7 @@ hts_status ok() {
     return HTS_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool is16bit(int32_t dt) { return dt == HTS_F16 || dt == HTS_BF16; }
-bool is_in(int32_t dt) { return is16bit(dt) || dt == HTS_FP8_E4M3; }
-int elem_bytes(int32_t dt) { return dt == HTS_FP8_E4M3 ? 1 : 2; }
-int ld_mult(int32_t dt) { return 16 / elem_bytes(dt); }   // leading dimensions: whole 16-byte chunks
-bool is_out(int32_t dt) { return dt == HTS_F16 || dt == HTS_BF16 || dt == HTS_F32; }
-
-hts_status check_desc(const hts_desc* d) {
-    if (!d) return fail(HTS_ERR_INVALID_ARG, "descriptor is NULL");
-    if (!is_in(d->dtype)) return fail(HTS_ERR_DTYPE, "dtype %d is not HTS_F16, HTS_BF16 or HTS_FP8_E4M3", d->dtype);
-    if (d->reserved != 0) return fail(HTS_ERR_INVALID_ARG, "descriptor reserved field must be 0");
-    if (d->N <= 0 || d->K <= 0) return fail(HTS_ERR_SHAPE, "N=%lld K=%lld must be positive", (long long)d->N,
-                                            (long long)d->K);
-    if (!((d->bn == 32 || d->bn == 64 || d->bn == 128) && (d->bk == 32 || d->bk == 64 || d->bk == 128)))
-        return fail(HTS_ERR_UNSUPPORTED, "tile %dx%d: bn and bk must each be 32, 64 or 128", d->bn, d->bk);
-    if (d->dtype == HTS_FP8_E4M3 && (d->bn != 128 || d->bk != 128))
-        return fail(HTS_ERR_UNSUPPORTED, "tile %dx%d: 8-bit weights use 128x128 tiles", d->bn, d->bk);
-    if (d->N % d->bn || d->K % d->bk)
-        return fail(HTS_ERR_SHAPE, "N=%lld K=%lld are not multiples of the %dx%d tile", (long long)d->N,
-                    (long long)d->K, d->bn, d->bk);
-    if ((double)d->N * (double)d->K >= 4294967296.0)
-        return fail(HTS_ERR_SHAPE, "N*K must be below 2^32 (32-bit value offsets)");
-    return HTS_OK;
-}
+const char* last_error() { return g_err; }
 
 hts_status check_ld(int64_t ld, int64_t minv, int mult, const char* name) {
     if (ld < minv) return fail(HTS_ERR_SHAPE, "%s=%lld is smaller than %lld", name, (long long)ld, (long long)minv);
@@ -102,6 +83,36 @@ hts_status debug_range(const void* p, uint64_t bytes, const char* name) {
     if (q < lo || q - lo + bytes > size)
         return fail(HTS_ERR_SHAPE, "HTS_DEBUG: %s needs %llu bytes; its allocation ends %llu bytes after it", name,
                     (unsigned long long)bytes, (unsigned long long)(q >= lo && q - lo <= size ? size - (q - lo) : 0));
+    return HTS_OK;
+}
+
+}  // namespace api
+}  // namespace hts
+
+namespace {
+
+using namespace hts::api;
+
+bool is_in(int32_t dt) { return is16bit(dt) || dt == HTS_FP8_E4M3; }
+int elem_bytes(int32_t dt) { return dt == HTS_FP8_E4M3 ? 1 : 2; }
+int ld_mult(int32_t dt) { return 16 / elem_bytes(dt); }   // leading dimensions: whole 16-byte chunks
+bool is_out(int32_t dt) { return dt == HTS_F16 || dt == HTS_BF16 || dt == HTS_F32; }
+
+hts_status check_desc(const hts_desc* d) {
+    if (!d) return fail(HTS_ERR_INVALID_ARG, "descriptor is NULL");
+    if (!is_in(d->dtype)) return fail(HTS_ERR_DTYPE, "dtype %d is not HTS_F16, HTS_BF16 or HTS_FP8_E4M3", d->dtype);
+    if (d->reserved != 0) return fail(HTS_ERR_INVALID_ARG, "descriptor reserved field must be 0");
+    if (d->N <= 0 || d->K <= 0) return fail(HTS_ERR_SHAPE, "N=%lld K=%lld must be positive", (long long)d->N,
+                                            (long long)d->K);
+    if (!((d->bn == 32 || d->bn == 64 || d->bn == 128) && (d->bk == 32 || d->bk == 64 || d->bk == 128)))
+        return fail(HTS_ERR_UNSUPPORTED, "tile %dx%d: bn and bk must each be 32, 64 or 128", d->bn, d->bk);
+    if (d->dtype == HTS_FP8_E4M3 && (d->bn != 128 || d->bk != 128))
+        return fail(HTS_ERR_UNSUPPORTED, "tile %dx%d: 8-bit weights use 128x128 tiles", d->bn, d->bk);
+    if (d->N % d->bn || d->K % d->bk)
+        return fail(HTS_ERR_SHAPE, "N=%lld K=%lld are not multiples of the %dx%d tile", (long long)d->N,
+                    (long long)d->K, d->bn, d->bk);
+    if ((double)d->N * (double)d->K >= 4294967296.0)
+        return fail(HTS_ERR_SHAPE, "N*K must be below 2^32 (32-bit value offsets)");
     return HTS_OK;
 }
 
@@ -431,7 +442,7 @@ const char* hts_status_string(int s) {
     }
 }
 
-const char* hts_last_error(void) { return g_err; }
+const char* hts_last_error(void) { return last_error(); }
 
 hts_status hts_pack_plan(const hts_desc* d, const uint8_t* tile_map_host, hts_tile* index_host, hts_sizes* sizes) {
     hts_status st = check_desc(d);
