@@ -276,6 +276,174 @@ hts_status hts_wanda_tile_cost(const hts_desc* d, const void* W, int64_t ldw,
 hts_status hts_wanda_map(int64_t T, const double* cost, int64_t n_sparse, uint8_t* map,
                          void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Around the products: what a decode step of a decoder block needs besides its seven linear
+ * layers -- the pages of a key-value cache, rotary positions, attention over the cache, and the
+ * norms between the products.  These steps are the architecture's, not the pruning method's (the
+ * pages prune the linear layers of LLaMA models); they let a block of hybrid products run whole.
+ * The conventions above hold: host checks before anything is enqueued, caller-owned buffers, no
+ * allocation, capturable in a HIP graph.  Index values that live in device memory (lengths, block
+ * tables, slots, positions) cannot be checked on the host; the kernels check every one against
+ * the sizes given here before using it, so a bad value never reaches memory outside the buffers.
+ * ------------------------------------------------------------------------------------------ */
+
+/* A paged key-value cache: `pages` pages of `page` tokens, each token holding `heads` heads of
+ * `dim` values.  Element (p, t, h, d) of K (and, with the same strides, of V) is at
+ * p*page_stride + t*token_stride + h*head_stride + d, in elements.  page: a power of two, 16 to
+ * 1024.  dim: a multiple of 8, 8 to 256.  Strides: multiples of 8, with no two elements at one
+ * place (any nesting of pages, tokens and heads; the stride of an axis of size 1 is not used).
+ * dtype: HTS_F16, HTS_BF16 or HTS_FP8_E4M3; an 8-bit cache holds value / scale, with one float
+ * scale per head (k_scale, v_scale; NULL = 1), which must be positive and finite. */
+typedef struct {
+    int64_t pages;
+    int32_t page, heads, dim, dtype;
+    int64_t page_stride, token_stride, head_stride;
+} hts_kv_desc;
+
+/* Device, asynchronous.  Block tables, slots and positions of one step, from request lengths.
+ * Request b has cached[b] tokens in the cache and adds added[b] (device int32[B]; negative counts
+ * as 0).  Its row of block_table (device int32 [B, ldt], `width` columns used) holds the pages of
+ * its cached tokens; the pages its new tokens open are taken from free_pages (device
+ * int32[n_free]) from entry *free_head on (device int32[1]; NULL = 0), in order of request, then
+ * page, and written behind the cached ones.  Every other entry of the table is left as it was.
+ * Where the free list has ended the entry is -1, and so is the slot of a token without a page.
+ *   lengths   : int32[B]        min(cached + added, width * page)
+ *   starts    : int32[B + 1]    first new token of each request in the step's token order
+ *   slots     : int64[tokens]   page id * page + place in the page, or -1 (no page, or the position
+ *                               lies past the table's width)
+ *   positions : int32[tokens]   the token's position in its request
+ *   head_out  : int32[1]        *free_head plus the pages the step opens (above n_free when the
+ *                               list was too short)
+ * Tokens past the step's last one, up to `tokens`, get slot and position -1: a step captured for
+ * `tokens` tokens runs any smaller batch.  Tokens past `tokens` are not written.  Sums past
+ * 2^31 - 1 saturate.  0 <= B <= 4096; width, ldt, n_free, tokens and B * width below 2^31; outputs must not
+ * overlap inputs or one another.  All pointers 4-byte aligned, slots 8-byte.
+ * cached, added, block_table and lengths may be NULL when B == 0, free_pages when n_free == 0,
+ * slots and positions when tokens == 0. */
+hts_status hts_kv_step(int64_t B, const int32_t* cached, const int32_t* added, int32_t page,
+                       const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                       int32_t* block_table, int64_t ldt, int64_t width, int64_t tokens,
+                       int32_t* lengths, int32_t* starts, int64_t* slots, int32_t* positions,
+                       int32_t* head_out, void* stream);
+
+/* Rotary positions.  Pair i of a head's first `rot` entries is turned by position * f_i.
+ *   HTS_ROPE_HALF        : pair i = entries i and i + rot/2
+ *   HTS_ROPE_INTERLEAVED : pair i = entries 2i and 2i + 1
+ * Entries from rot on are copied. */
+enum { HTS_ROPE_HALF = 0, HTS_ROPE_INTERLEAVED = 1 };
+
+/* f_i = theta^(-2i/rot), i < rot/2, scaled for contexts longer than the trained one by `factor`:
+ *   HTS_ROPE_PLAIN      : f_i (factor must be 1)
+ *   HTS_ROPE_LINEAR     : f_i / factor
+ *   HTS_ROPE_BASE       : theta * factor^(rot / (rot - 2)) in place of theta
+ *   HTS_ROPE_RAMP       : f_i * (c + (1 - c) / factor), c = (n_i - low) / (high - low) clamped to
+ *                         0..1, n_i = context * f_i / 2 pi the pair's turns over the trained context
+ *   HTS_ROPE_RAMP_PAIRS : the same with c falling linearly over the pair index from 1 at
+ *                         floor(p(high)) to 0 at ceil(p(low)), both clamped to 0..rot - 1, where
+ *                         p(n) = rot * ln(context / 2 pi n) / (2 ln theta)
+ * context, low and high (0 < low < high) are used by the two ramps only. */
+enum { HTS_ROPE_PLAIN = 0, HTS_ROPE_LINEAR = 1, HTS_ROPE_BASE = 2, HTS_ROPE_RAMP = 3, HTS_ROPE_RAMP_PAIRS = 4 };
+typedef struct {
+    int32_t rot, rule;
+    double theta, factor, context, low, high;
+} hts_rope_scaling;
+
+/* Host only.  turns_host[i] = f_i / 2 pi (turns per position), i < rot/2, in 64 bits; the caller
+ * copies it to the device once.  rot: a multiple of 8, 8 to 256; theta > 1; factor >= 1. */
+hts_status hts_rope_plan(const hts_rope_scaling* s, double* turns_host);
+
+/* dtype HTS_F16 or HTS_BF16; dim a multiple of 8, 8 to 256; rot a multiple of 8, 8 to dim;
+ * magnitude: factor on the rotated entries (1 for none). */
+typedef struct {
+    int32_t dtype, layout, dim, rot, q_heads, k_heads;
+    float magnitude;
+    int32_t reserved;          /* must be 0 */
+} hts_rope_desc;
+
+/* Device, asynchronous.  Q_out = rotated Q [T, q_heads*dim] and K_out = rotated K
+ * [T, k_heads*dim], each row by its position (device int32[T]; int32 covers any context).  The
+ * angle is reduced to one turn in 64 bits, the rotation is 32-bit, rounded once.  A row whose
+ * position is negative is not written.  Q_out may be Q and K_out may be K (same leading
+ * dimension); q_heads or k_heads may be 0 (its pointers are not used).  turns: device
+ * double[rot/2] from hts_rope_plan, 8-byte aligned.  Matrices 16-byte aligned, leading dimensions
+ * multiples of 8. */
+hts_status hts_rope(const hts_rope_desc* d, const double* turns, int64_t T, const int32_t* positions,
+                    const void* Q, int64_t ldq, void* Q_out, int64_t ldqo,
+                    const void* K, int64_t ldk, void* K_out, int64_t ldko, void* stream);
+
+/* Device, asynchronous.  hts_rope with the rotated K and the V [T, k_heads*dim] written to the
+ * paged cache instead: token t to slot slots[t] (device int64[T]; page id * page + place).  A
+ * 16-bit cache has the input's type; an 8-bit one receives value / scale rounded once to E4M3
+ * (magnitudes past 448 become 448, NaN stays NaN).  A token whose slot is outside
+ * [0, pages * page) is not written to the cache; its q is still rotated.  A token whose position
+ * is negative is skipped whole.  Slots must differ from one another: of two tokens with one slot
+ * either may be kept, in parts.  k_heads and dim are the cache's.  Q_out may be Q. */
+hts_status hts_rope_cache(const hts_rope_desc* d, const double* turns, int64_t T, const int32_t* positions,
+                          const int64_t* slots, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo,
+                          const void* K, int64_t ldk, const void* V, int64_t ldv, const hts_kv_desc* kv,
+                          void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                          void* stream);
+
+/* Device, asynchronous.  Attention of one new token per request over the paged cache.  For request
+ * b and query head h (cache head h / (q_heads / kv->heads)), over the tokens t in
+ * [max(0, L - window), L), L = lengths[b] (device int32[B], clamped to 0 .. width*page; window 0 =
+ * all), whose block-table entry names a page of the cache (other tokens are left out):
+ *     s_t = scale * q . k_t,  O = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m),  m = max_t s_t
+ * with K and V multiplied by their head's scale for an 8-bit cache.  Scores, maximum, sums and
+ * accumulators are 32-bit; O is rounded once to dtype.  A request with no token (or only scores of
+ * minus infinity) gets zeros.  lse (float [B, q_heads], or NULL) receives m + ln sum e^(s_t - m),
+ * minus infinity for such a request: two calls over parts of a context can be joined by it.
+ * What the cache holds past a request's tokens is never used (NaN there does no harm).
+ * Q, O: [B, q_heads*dim] in dtype (HTS_F16 / HTS_BF16), 16-byte aligned, leading dimensions
+ * multiples of 8; O may be Q.  The cache has dtype or HTS_FP8_E4M3.  q_heads is a multiple of
+ * kv->heads.  B <= 65535.  block_table: device int32 [B, ldt], `width` columns used.
+ * workspace: hts_paged_attn_workspace() bytes (16-byte aligned); the length is then split over
+ * workgroups and joined by a second kernel in a fixed order.  With less, or NULL, each request and
+ * head runs unsplit.  Results are deterministic for given lengths, shape and workspace size.
+ * Calls that share a workspace must not overlap. */
+hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_kv_desc* kv,
+                          const void* Q, int64_t ldq, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale,
+                          const int32_t* block_table, int64_t ldt, int64_t width, const int32_t* lengths,
+                          float scale, int64_t window, void* O, int64_t ldo, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Host only.  Bytes of the optional workspace of hts_paged_attn for these sizes (0 where no call
+ * of them is split). */
+hts_status hts_paged_attn_workspace(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t width,
+                                    int64_t window, size_t* bytes);
+
+/* Norms around a block.  HTS_NORM_RMS: x / sqrt(mean(x^2) + eps); HTS_NORM_LAYER:
+ * (x - mean(x)) / sqrt(var(x) + eps), both over the row, then * weight + bias. */
+enum { HTS_NORM_NONE = 0, HTS_NORM_RMS = 1, HTS_NORM_LAYER = 2 };
+enum { HTS_GATE_PLAIN = 0, HTS_GATE_SIGMOID = 1, HTS_GATE_SILU = 2 };
+
+/* dtype: HTS_F16 or HTS_BF16, of the block's output, gate, weights, biases and Y; r_dtype: of the
+ * residual stream, dtype or HTS_F32. */
+typedef struct {
+    int32_t dtype, r_dtype;
+    int32_t post, pre;         /* HTS_NORM_*: the norm of the block's output, the norm of the sum */
+    float post_eps, pre_eps;
+    float scale;               /* residual scale */
+    int32_t gate_act;          /* HTS_GATE_*: what the gate goes through */
+} hts_norm_desc;
+
+/* Device, asynchronous.  The step between two blocks, one pass over the rows:
+ *     R' = R + scale * act(gate) * post(block)        Y = pre(R')
+ * block [M,N] (ldb) or NULL (Y = pre(R)); gate NULL (none), or [M,N] with leading dimension ldg,
+ * ldg = 0 for one row shared by all; R [M,N] (ldr) or NULL (zero); R_out (ldro) receives R' rounded
+ * to r_dtype, or NULL; Y (ldy) receives pre(R') in dtype, from the unrounded R', or NULL.  One of
+ * block and R, and one of R_out and Y, must be given; gate and post need block.  weights and
+ * biases: N entries, 16-byte aligned, NULL = ones and zeros.  Sums are 32-bit; a layer norm's
+ * variance is summed around the mean.  R_out may be R, and Y may be block, a [M,N] gate, or
+ * an R in dtype that R_out does not keep (same pointer and leading dimension: each entry is read
+ * before it is written); other overlaps are not allowed.  N a multiple of 8, 8 to 32768; matrices 16-byte
+ * aligned, leading dimensions >= N and multiples of 8.  M == 0 is a no-op. */
+hts_status hts_residual_norm(const hts_norm_desc* d, int64_t M, int64_t N, const void* block, int64_t ldb,
+                             const void* post_weight, const void* post_bias, const void* gate, int64_t ldg,
+                             const void* R, int64_t ldr, const void* pre_weight, const void* pre_bias,
+                             void* R_out, int64_t ldro, void* Y, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,601 @@
+"""GPU parity of the steps around the products: page step, rotary positions with the cache write, paged
+attention, residual norm -- each against its 64-bit form (serving_ref), with what must stay as it was
+held in canary values.  Tolerances: half a rounding step of the output (finfo.eps / 2 relative) plus the
+bound on the 32-bit arithmetic that the reference carries."""
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as ref
+import tile_gemm_amd as hts
+from helpers import DEV, say
+
+pytestmark = pytest.mark.gpu
+TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32, "fp8": torch.float8_e4m3fn}
+
+
+def f64(t):
+    return t.float().double().cpu().numpy() if t.dtype != torch.float64 else t.cpu().numpy()
+
+
+def normal(g, shape, dtype, sigma=1.0):
+    return torch.from_numpy(g.standard_normal(shape).astype(np.float32) * np.float32(sigma)).to(DEV).to(TORCH[dtype])
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def strided(t, pad, fill=7.0):
+    """The same matrix with a leading dimension pad entries longer, and the buffer it lies in."""
+    big = torch.full((t.shape[0], t.shape[1] + pad), fill, dtype=t.dtype, device=DEV)
+    big[:, :t.shape[1]] = t
+    return big[:, :t.shape[1]], big
+
+
+# ---- page step -------------------------------------------------------------
+
+def _step_case(B, page, width, seed, mode):
+    g = np.random.default_rng(seed)
+    cap = width * page
+    cached = g.integers(0, max(1, cap - page), B)
+    added = g.integers(0, 3 * page, B) * (g.random(B) < 0.7)
+    if mode == "decode":
+        added = np.ones(B, np.int64)
+    if mode == "wild":                       # negative counts, lengths past the row, past 32 bits when added up
+        cached = np.where(g.random(B) < 0.3, g.integers(-50, 2 * cap, B), cached)
+        cached = np.where(g.random(B) < 0.1, 2 ** 31 - 1, cached)
+        added = np.where(g.random(B) < 0.2, -3, added)
+    n_free = B * width if mode != "short" else max(1, B // 2)
+    free = g.permutation(n_free + 5)[:n_free]
+    if mode == "wild":
+        free = np.where(g.random(n_free) < 0.1, -7, free)
+    table = g.integers(-1, 1000, (B, width + 3))
+    tokens = int(np.maximum(added, 0).sum()) + {"decode": 0, "mixed": 9, "short": 5, "wild": 40}[mode]
+    if mode == "mixed" and B % 2:
+        tokens = max(0, tokens // 2)         # a capacity below the batch's tokens
+    return cached, added, free, table, tokens
+
+
+@pytest.mark.parametrize("mode", ["decode", "mixed", "short", "wild"])
+@pytest.mark.parametrize("B,page,width", [(1, 16, 1), (3, 16, 40), (64, 16, 7), (65, 64, 5), (257, 16, 9),
+                                          (1000, 128, 3), (4096, 1024, 2)])
+def test_kv_step(B, page, width, mode):
+    cached, added, free, table, tokens = _step_case(B, page, width, B + page, mode)
+    head = {"decode": 0, "mixed": 2, "short": 0, "wild": -4}[mode]
+    say(f"[kv_step] B={B} page={page} width={width} {mode} tokens={tokens}")
+    t = i32(table)
+    st = hts.kv_step(i32(cached), i32(added), i32(free), t[:, :width], page, tokens,
+                     free_head=None if mode == "decode" else i32([head]))
+    want = ref.kv_step(cached.tolist(), added.tolist(), page, free.tolist(), head, table.tolist(), width, tokens)
+    got = (t.cpu().tolist(), st.lengths.cpu().tolist(), st.starts.cpu().tolist(), st.slots.cpu().tolist(),
+           st.positions.cpu().tolist(), int(st.head))
+    for name, a, b in zip(("table", "lengths", "starts", "slots", "positions", "head"), got, want):
+        assert a == b, name
+
+
+def test_kv_step_of_no_requests_and_no_tokens():
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    st = hts.kv_step(e, e, e, torch.empty((0, 4), dtype=torch.int32, device=DEV), 16, 5, free_head=i32([3]))
+    assert st.starts.tolist() == [0] and st.slots.tolist() == [-1] * 5 and st.positions.tolist() == [-1] * 5
+    assert int(st.head) == 3
+    t = i32([[5, -1, -1]])
+    st = hts.kv_step(i32([16]), i32([17]), i32([8, 9]), t, 16, 0)
+    assert t.tolist() == [[5, 8, 9]] and st.lengths.tolist() == [33] and st.starts.tolist() == [0, 17]
+
+
+def test_kv_step_grows_a_running_batch():
+    # steps one after another, each from the last one's lengths and head: every token keeps its slot
+    B, page, width = 5, 16, 6
+    free = torch.randperm(B * width, device=DEV).int()
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    cached, head = torch.zeros(B, dtype=torch.int32, device=DEV), i32([0])
+    seen = {}
+    for add in ([20, 1, 0, 33, 16], [1] * 5, [1] * 5, [0, 15, 40, 1, 1], [1] * 5):
+        st = hts.kv_step(cached, i32(add), free, table, page, sum(add), free_head=head)
+        b = np.repeat(np.arange(B), add)
+        for who, pos, slot in zip(b, st.positions.tolist(), st.slots.tolist()):
+            assert slot >= 0 and (int(who), pos) not in seen and slot not in seen.values()
+            seen[(int(who), pos)] = slot
+        cached, head = st.lengths, st.head
+        rows = table.cpu().numpy()
+        for (who, pos), slot in seen.items():
+            assert rows[who, pos // page] * page + pos % page == slot
+    assert cached.tolist() == [23, 19, 43, 37, 20]
+
+
+# ---- rotary ----------------------------------------------------------------
+
+ROPE = [  # dim, rot, layout, q heads, k heads, tokens
+    (128, 128, "half", 32, 32, 1), (128, 128, "interleaved", 8, 2, 37), (64, 64, "half", 3, 1, 5),
+    (80, 40, "half", 5, 5, 9), (96, 48, "interleaved", 4, 1, 3), (256, 64, "half", 2, 1, 300),
+    (256, 256, "interleaved", 2, 2, 4), (8, 8, "half", 1, 1, 2), (192, 16, "half", 3, 2, 17),
+    (88, 24, "interleaved", 7, 3, 65), (128, 8, "half", 40, 8, 2),
+]
+
+
+def _positions(g, T):
+    p = g.integers(0, 100000, T)
+    far = [0, 1, 2 ** 31 - 1, 1000003, 131071]
+    p[:min(T, 5)] = far[:min(T, 5)]
+    return p
+
+
+# The angle in turns is below 2^29; the plan's and the product's roundings leave at most 2^-23 of a turn
+# there, the reduced turn's own rounding and the sine's 2^-24 each: under 2^-20 in radians with the factor
+# 2 pi, and four more roundings of 2^-24 in the rotation.
+TURN = 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,rot,layout,hq,hk,T", ROPE)
+def test_rope(dtype, dim, rot, layout, hq, hk, T):
+    g = np.random.default_rng(dim + rot + T)
+    q, k = normal(g, (T, hq * dim), dtype), normal(g, (T, hk * dim), dtype)
+    pos = _positions(g, T)
+    if T > 8:
+        pos[T // 2] = -1                       # a skipped row
+    say(f"[rope] {dtype} dim={dim} rot={rot} {layout} {hq}/{hk} T={T}")
+    plan = hts.rope_plan(dim, rot, theta=500000.0, layout=layout, rule="linear", factor=1.5, magnitude=1.25, device=DEV)
+    turns = ref.rope_turns(rot, 500000.0, "linear", 1.5)
+    qs, ks = strided(q, 24)[0], strided(k, 8)[0]
+    qo, qbig = strided(torch.full_like(q, 3.0), 16)
+    ko, kbig = strided(torch.full_like(k, 3.0), 40)
+    hts.rope(qs, ks, i32(pos), plan, q_out=qo, k_out=ko)
+    for x, got, big in ((q, qo, qbig), (k, ko, kbig)):
+        want, size = ref.rope(f64(x), pos, turns, dim, layout, 1.25)
+        live = pos >= 0
+        err = np.abs(f64(got) - want)
+        tol = ref.EPS[dtype] / 2 * np.abs(want) + TURN * size + ref.TINY[dtype]
+        assert np.all(err[live] <= tol[live]), float((err - tol)[live].max())
+        assert np.all(f64(got)[~live] == 3.0)
+        assert torch.all(big[:, x.shape[1]:] == 7.0)
+    # in place, q alone and k alone: the same bits
+    q2, k2 = q.clone(), k.clone()
+    hts.rope(q2, None, i32(pos), plan)
+    hts.rope(None, k2, i32(pos), plan)
+    live = torch.from_numpy(pos >= 0).to(DEV)
+    assert torch.equal(q2[live], qo[live]) and torch.equal(k2[live], ko[live])
+    assert torch.equal(q2[~live], q[~live])
+
+
+@pytest.mark.parametrize("cache_dtype", ["same", "fp8"])
+@pytest.mark.parametrize("order", ["token", "head"])
+@pytest.mark.parametrize("dim,rot,layout,hq,hk,T", ROPE)
+def test_rope_cache(dim, rot, layout, hq, hk, T, order, cache_dtype):
+    dtype = "bf16" if T % 2 else "f16"
+    g = np.random.default_rng(dim * 3 + rot + T)
+    page = 16 if T % 3 else 32
+    pages = -(-T // page) + 2
+    qkv = normal(g, (T, (hq + 2 * hk) * dim), dtype, 3.0)
+    q, k, v = qkv[:, :hq * dim], qkv[:, hq * dim:(hq + hk) * dim], qkv[:, (hq + hk) * dim:]
+    pos = _positions(g, T)
+    slots = g.permutation(pages * page)[:T]
+    if T > 8:
+        pos[3], slots[4], slots[5], slots[6] = -1, -1, pages * page, 2 ** 40
+    ct = dtype if cache_dtype == "same" else "fp8"
+    ks = vs = None
+    if ct == "fp8":
+        ks = torch.from_numpy(g.uniform(0.01, 2.0, hk).astype(np.float32)).to(DEV)
+        vs = torch.from_numpy(g.uniform(0.01, 2.0, hk).astype(np.float32)).to(DEV)
+    cache = hts.kv_cache(pages, page, hk, dim, TORCH[ct], DEV, order, ks, vs)
+    for c in (cache.k, cache.v):
+        c.view(torch.uint8).fill_(0x11)
+    before = [c.view(torch.uint8).clone() for c in (cache.k, cache.v)]
+    say(f"[rope_cache] {dtype} cache={ct} {order} dim={dim} rot={rot} {layout} {hq}/{hk} T={T}")
+    plan = hts.rope_plan(dim, rot, layout=layout, device=DEV)
+    qo = torch.full((T, hq * dim), 3.0, dtype=TORCH[dtype], device=DEV)
+    hts.rope_cache(q, k, v, i32(pos), torch.from_numpy(slots).to(DEV), plan, cache, q_out=qo)
+    turns = ref.rope_turns(rot)
+    live = pos >= 0
+    want, size = ref.rope(f64(q), pos, turns, dim, layout, 1.0)
+    tol = ref.EPS[dtype] / 2 * np.abs(want) + TURN * size + ref.TINY[dtype]
+    assert np.all((np.abs(f64(qo) - want) <= tol)[live]) and np.all(f64(qo)[~live] == 3.0)
+    put = live & (slots >= 0) & (slots < pages * page)
+    where = (slots[put] // page, slots[put] % page)
+    want, size = ref.rope(f64(k), pos, turns, dim, layout, 1.0)
+    for c, x, sz, s in ((cache.k, want, size, ks), (cache.v, f64(v), np.zeros_like(size), vs)):
+        got = f64(c)[where]
+        x, sz = x.reshape(T, hk, dim)[put], sz.reshape(T, hk, dim)[put]
+        if ct == "fp8":
+            sc = np.ones(hk) if s is None else f64(s)
+            x, sz = x / sc[:, None], sz / sc[:, None]
+            x = np.clip(x, -448.0, 448.0)
+            # half a step of e4m3 (2^-4 of the value, 2^-10 among its subnormals) and the division's rounding
+            tol = 2.0 ** -4 * np.abs(x) + 2.0 ** -10 + TURN * sz + 2.0 ** -23 * np.abs(x)
+        else:
+            tol = ref.EPS[dtype] / 2 * np.abs(x) + TURN * sz + ref.TINY[dtype]
+        assert np.all(np.abs(got - x) <= tol)
+    # nothing but those slots was written
+    for c, b in zip((cache.k, cache.v), before):
+        now = c.view(torch.uint8).clone()
+        now[torch.from_numpy(where[0]).to(DEV), torch.from_numpy(where[1]).to(DEV)] = 0x11
+        assert torch.equal(now, b)
+
+
+def test_e4m3_cache_rounds_to_nearest_even_and_saturates():
+    # v is stored unturned: every 16-bit value in order of the format, against torch's own E4M3 conversion
+    bits = torch.arange(65536, dtype=torch.int32, device=DEV).to(torch.int16)
+    for dt in (torch.bfloat16, torch.float16):
+        v = bits.view(dt).view(256, 256)
+        k = torch.zeros_like(v)
+        cache = hts.kv_cache(16, 16, 1, 256, torch.float8_e4m3fn, DEV)
+        plan = hts.rope_plan(256, 8, device=DEV)
+        hts.rope_cache(k.clone(), k, v, torch.zeros(256, dtype=torch.int32, device=DEV),
+                       torch.arange(256, device=DEV), plan, cache)
+        got = cache.v.reshape(256, 256).float()
+        f = v.float()
+        want = f.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).float()
+        assert torch.equal(torch.isnan(got), torch.isnan(f))
+        ok = ~torch.isnan(f)
+        assert torch.equal(got[ok], want[ok])
+
+
+# ---- attention -------------------------------------------------------------
+
+ATTN = [  # dim, q heads, k heads, page, order, cache, window, lengths
+    (128, 32, 32, 16, "token", "same", 0, [1]),
+    (128, 32, 8, 16, "token", "same", 0, [0, 1, 15, 16, 17, 31, 32, 33, 100, 257]),
+    (128, 8, 8, 64, "head", "same", 0, [63, 64, 65, 0, 500]),
+    (128, 40, 8, 32, "head", "fp8", 0, [7, 0, 300, 1111]),
+    (64, 14, 2, 16, "token", "same", 0, [5, 129, 640]),
+    (64, 6, 3, 128, "head", "fp8", 0, [1, 128, 129, 1000]),
+    (80, 5, 5, 16, "token", "same", 0, [33, 1, 90]),
+    (96, 12, 4, 16, "head", "fp8", 0, [48, 700]),
+    (192, 8, 1, 256, "token", "same", 0, [2, 255, 256, 257]),
+    (256, 16, 1, 16, "token", "same", 0, [0, 400, 3]),
+    (256, 6, 2, 1024, "head", "fp8", 0, [1500, 1]),
+    (8, 4, 4, 16, "token", "same", 0, [40, 2]),
+    (8, 9, 3, 16, "head", "fp8", 0, [40, 2]),
+    (128, 40, 2, 16, "token", "same", 0, [700, 50, 0]),      # more than 16 query heads to a cache head
+    (104, 33, 1, 32, "head", "same", 0, [513, 64]),
+    (128, 8, 2, 16, "token", "same", 1, [50, 0, 1, 3000]),   # windows
+    (128, 8, 2, 32, "head", "fp8", 100, [99, 100, 101, 2500]),
+    (64, 4, 4, 16, "token", "same", 1000, [5000, 999, 17]),
+    (128, 8, 1, 16, "token", "same", 0, [20000, 3, 0, 9000]),  # lengths that are split
+    (128, 16, 2, 64, "token", "fp8", 0, [12345]),
+    (72, 3, 3, 16, "head", "same", 5000, [16384, 40]),
+]
+
+
+def _attn_case(dim, hq, hk, page, order, cache, lengths, dtype, seed, spare=2):
+    g = np.random.default_rng(seed)
+    B, width = len(lengths), -(-max(max(lengths), 1) // page) + 1
+    need = [-(-n // page) for n in lengths]
+    pages = sum(need) + spare
+    ct = dtype if cache == "same" else "fp8"
+    ks = vs = None
+    if ct == "fp8":
+        ks = torch.from_numpy(g.uniform(0.2, 2.0, hk).astype(np.float32)).to(DEV)
+        vs = torch.from_numpy(g.uniform(0.2, 2.0, hk).astype(np.float32)).to(DEV)
+    c = hts.kv_cache(pages, page, hk, dim, TORCH[ct], DEV, order, ks, vs)
+    # every place holds NaN but those of the requests' tokens
+    c.k.view(torch.uint8).fill_(0x7F if ct == "fp8" else 0xFF)
+    c.v.view(torch.uint8).fill_(0x7F if ct == "fp8" else 0xFF)
+    ids = g.permutation(pages)
+    table = np.full((B, width + 2), -1)
+    at = 0
+    gg = torch.Generator(device=DEV)
+    gg.manual_seed(seed)
+    for b, n in enumerate(lengths):
+        table[b, :need[b]] = ids[at:at + need[b]]
+        at += need[b]
+        if n:
+            t = torch.arange(n, device=DEV)
+            rows = torch.from_numpy(table[b]).to(DEV)[t // page]
+            for x in (c.k, c.v):
+                val = torch.randn((n, hk, dim), generator=gg, device=DEV).to(TORCH[ct])
+                if ct == "fp8":
+                    x.view(torch.uint8)[rows, t % page] = val.view(torch.uint8)
+                else:
+                    x[rows, t % page] = val
+    q = normal(g, (B, hq * dim), dtype)
+    return q, c, table, width
+
+
+def _check_attn(q, c, table, width, lengths, hq, window, scale, out, lse, dtype):
+    k, v = f64(c.k), f64(c.v)
+    if c.k_scale is not None:
+        k, v = k * f64(c.k_scale)[:, None], v * f64(c.v_scale)[:, None]
+    B = len(lengths)
+    want, wl, err, el = ref.attn(f64(q).reshape(B, hq, c.dim), k, v, table[:, :width], lengths, c.page, scale, window,
+                                 c.heads)
+    got = f64(out).reshape(B, hq, c.dim)
+    tol = ref.EPS[dtype] / 2 * np.abs(want) + err + ref.TINY[dtype]
+    bad = np.abs(got - want) - tol
+    assert np.all(bad <= 0), f"out off by {float(np.nanmax(bad)):.3e} past its tolerance (NaN: {np.isnan(got).sum()})"
+    if lse is not None:
+        g = f64(lse)
+        empty = np.isinf(wl)
+        assert np.array_equal(g[empty], wl[empty])
+        assert np.all(np.abs(g - wl)[~empty] <= el[~empty]), float((np.abs(g - wl) - el)[~empty].max())
+    return want
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,hq,hk,page,order,cache,window,lengths", ATTN)
+def test_paged_attn(dim, hq, hk, page, order, cache, window, lengths, dtype):
+    q, c, table, width = _attn_case(dim, hq, hk, page, order, cache, lengths, dtype, dim + hq + page)
+    say(f"[attn] {dtype} dim={dim} {hq}/{hk} page={page} {order} {cache} window={window} lengths={lengths}")
+    B = len(lengths)
+    qs = strided(q, 16)[0]
+    out, big = strided(torch.full_like(q, 5.0), 8)
+    lse = torch.empty((B, hq), dtype=torch.float32, device=DEV)
+    t = i32(table)[:, :width]
+    scale = 0.7 * dim ** -0.5
+    hts.paged_attn(qs, c, t, i32(lengths), scale=scale, window=window, out=out, lse=lse)
+    _check_attn(q, c, table, width, lengths, hq, window, scale, out, lse, dtype)
+    assert torch.all(big[:, q.shape[1]:] == 7.0)
+    # the same call again: the same bits; in place, and unsplit for lack of a workspace: within the tolerance
+    again = hts.paged_attn(q, c, t, i32(lengths), scale=scale, window=window)
+    assert torch.equal(again, out)
+    q2 = q.clone()
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    hts.paged_attn(q2, c, t, i32(lengths), scale=scale, window=window, out=q2, workspace=small)
+    _check_attn(q, c, table, width, lengths, hq, window, scale, q2, None, dtype)
+
+
+def test_paged_attn_leaves_out_what_no_page_holds():
+    # entries of -1, ids past the cache and lengths past the table (and negative) within the requests
+    lengths = [200, 90, 33, 64]
+    q, c, table, width = _attn_case(128, 8, 2, 16, "token", "same", lengths, "bf16", 5)
+    table[0, 3], table[0, 4], table[1, 0:6], table[2, 0] = -1, 10 ** 6, -5, 2 ** 31 - 1
+    given = [200, 90, 33, -64]
+    lse = torch.empty((4, 8), dtype=torch.float32, device=DEV)
+    out = hts.paged_attn(q, c, i32(table)[:, :width], i32(given), scale=0.1, lse=lse)
+    want = _check_attn(q, c, table, width, given, 8, 0, 0.1, out, lse, "bf16")
+    assert np.all(want[1] == 0) and np.all(want[3] == 0) and np.any(want[2] != 0)
+    # a length past what the table's width holds ends there
+    cut = -(-64 // 16)
+    out = hts.paged_attn(q[3:], c, i32(table)[3:, :cut], i32([10 ** 9]), scale=0.1)
+    _check_attn(q[3:], c, table[3:], cut, [64], 8, 0, 0.1, out, None, "bf16")
+
+
+def test_paged_attn_far_offsets():
+    # an 8-bit cache of 5 GB: offsets past 2^32 elements
+    page, hk, dim = 64, 8, 128
+    pages = (5 << 30) // (page * hk * dim)
+    k = torch.empty((pages, page, hk, dim), dtype=torch.float8_e4m3fn, device=DEV)
+    v = torch.empty_like(k)
+    g = np.random.default_rng(1)
+    use = [pages - 1, 0, pages - 2, pages // 2, 70000]
+    small = hts.kv_cache(5, page, hk, dim, torch.float8_e4m3fn, DEV)
+    for big, sm in ((k, small.k), (v, small.v)):
+        sm.copy_(normal(g, sm.shape, "f32").to(torch.float8_e4m3fn))
+        for i, p in enumerate(use):
+            big.view(torch.uint8)[p] = sm.view(torch.uint8)[i]
+    q = normal(g, (1, 16 * dim), "bf16")
+    n = i32([5 * page - 3])
+    a = hts.paged_attn(q, hts.KVCache(k, v), i32([use]), n)
+    b = hts.paged_attn(q, small, i32([[0, 1, 2, 3, 4]]), n)
+    assert torch.equal(a, b) and bool((a != 0).any())
+    # and the cache write of the rotary step there
+    plan = hts.rope_plan(dim, device=DEV)
+    x = normal(g, (2, hk * dim), "bf16")
+    slots = torch.tensor([(pages - 1) * page + 5, 3 * page], device=DEV)
+    hts.rope_cache(x.clone(), x, x, i32([9, 10]), slots, plan, hts.KVCache(k, v))
+    hts.rope_cache(x.clone(), x, x, i32([9, 10]), torch.tensor([5, 64], device=DEV), plan, small)
+    assert torch.equal(k.view(torch.uint8)[pages - 1, 5], small.k.view(torch.uint8)[0, 5])
+    assert torch.equal(v.view(torch.uint8)[3, 0], small.v.view(torch.uint8)[1, 0])
+
+
+def test_paged_attn_extreme_scores():
+    # scores in the tens of thousands, all equal scores, and rows whose scores are all minus infinity
+    page, dim = 16, 128
+    c = hts.kv_cache(3, page, 1, dim, torch.float16, DEV)
+    g = np.random.default_rng(2)
+    c.k.copy_(normal(g, c.k.shape, "f16", 100.0))
+    c.v.copy_(normal(g, c.v.shape, "f16"))
+    table = np.array([[2, 0, 1]])
+    q = normal(g, (1, 4 * dim), "f16", 30.0)
+    q[0, dim:2 * dim] = 0
+    out = hts.paged_attn(q, c, i32(table), i32([40]), scale=1.0)
+    k, v = f64(c.k), f64(c.v)
+    want, _, err, _ = ref.attn(f64(q).reshape(1, 4, dim), k, v, table, [40], page, 1.0, 0, 1)
+    tol = ref.EPS["f16"] / 2 * np.abs(want) + err + ref.TINY["f16"]
+    assert np.all(np.abs(f64(out).reshape(1, 4, dim) - want) <= tol)
+    c.k[2, 5, 0, 0] = float("inf")            # q.k = -inf for that token alone: it gets no weight
+    q = torch.zeros((1, dim), dtype=torch.float16, device=DEV)
+    q[0, 0] = -1.0
+    lse = torch.empty((1, 1), device=DEV)
+    out = hts.paged_attn(q, c, i32(table), i32([40]), scale=1.0, lse=lse)
+    kk = k.copy()
+    kk[2, 5] = 0
+    t = np.array([i for i in range(40) if i != 5])
+    ids = table[0, t // page]
+    s = -kk[ids, t % page, 0, 0]
+    p = np.exp(s - s.max())
+    want = p @ v[ids, t % page, 0] / p.sum()
+    assert np.all(np.abs(f64(out)[0] - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -14 * np.abs(v).max())
+    c.k[..., 0] = float("inf")                # every score minus infinity: no weight at all
+    out = hts.paged_attn(q, c, i32(table), i32([40]), scale=1.0, lse=lse)
+    assert torch.all(out == 0) and float(lse) == -np.inf
+    c.k.zero_()
+    c.v[2, 7, 0, 3] = float("nan")            # NaN in a token that counts does show
+    out = hts.paged_attn(q, c, i32(table), i32([40]), scale=1.0)
+    assert bool(torch.isnan(out[0, 3])) and int(torch.isnan(out).sum()) == 1
+
+
+@pytest.mark.parametrize("lengths", [[100, 3], [9000, 70, 0]])
+def test_paged_attn_in_a_graph(lengths):
+    # captured once at one set of lengths, replayed at others with eager work in between
+    q, c, table, width = _attn_case(128, 16, 2, 16, "token", "same", lengths, "bf16", 11)
+    t, n = i32(table)[:, :width].contiguous(), i32(lengths)
+    eager = {}
+    variants = [lengths, [x // 2 for x in lengths], [0] * len(lengths), [max(1, x - 1) for x in lengths]]
+    for i, ls in enumerate(variants):
+        eager[i] = hts.paged_attn(q, c, t, i32(ls)).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        hts.paged_attn(q, c, t, n)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = hts.paged_attn(q, c, t, n)
+    for rep in range(2):
+        for i, ls in enumerate(variants):
+            n.copy_(i32(ls))
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager[i]), f"replay {rep} at lengths {ls}"
+            assert torch.equal(hts.paged_attn(q, c, t, i32(ls)), eager[i])
+
+
+def test_steps_on_another_stream():
+    lengths = [9000, 70, 0]
+    q, c, table, width = _attn_case(128, 16, 2, 16, "token", "same", lengths, "bf16", 12)
+    t, n = i32(table)[:, :width], i32(lengths)
+    want = hts.paged_attn(q, c, t, n)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [hts.paged_attn(q, c, t, n, stream=s), hts.paged_attn(q, c, t, n, stream=s.cuda_stream)]
+    x = normal(np.random.default_rng(0), (5, 64), "bf16")
+    torch.cuda.synchronize()
+    r, y = hts.residual_norm(x, x, pre=hts.Norm("rms"), stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+    r2, y2 = hts.residual_norm(x, x, pre=hts.Norm("rms"))
+    assert torch.equal(r, r2) and torch.equal(y, y2)
+
+
+# ---- norm ------------------------------------------------------------------
+
+NORM = [  # post, pre, gate, act, scale, residual
+    ("none", "rms", "none", "none", 1.0, "same"), ("rms", "rms", "channel", "none", 0.5, "f32"),
+    ("layer", "layer", "token", "sigmoid", 1.0, "same"), ("rms", "none", "token", "silu", -1.5, "f32"),
+    ("none", "layer", "channel", "silu", 0.25, "same"), ("layer", "rms", "none", "none", 3.0, "f32"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N", [(1, 8), (3, 64), (130, 128), (5, 520), (9, 1000), (2, 2048), (7, 2056), (300, 4096),
+                                 (3, 4104), (4, 5120), (2, 8192), (3, 8200), (2, 16384), (2, 32768)])
+@pytest.mark.parametrize("post,pre,gate,act,scale,res", NORM)
+def test_residual_norm(M, N, post, pre, gate, act, scale, res, dtype):
+    g = np.random.default_rng(M + N)
+    rt = dtype if res == "same" else "f32"
+    x, r = normal(g, (M, N), dtype, 2.0), normal(g, (M, N), rt, 3.0) + 0.5
+    x[0] = 0                                   # a row of zeros
+    if M > 2:
+        r[1], x[1] = 5.0, 1.0                  # rows of one value
+    gt = None if gate == "none" else normal(g, (N,) if gate == "channel" else (M, N), dtype)
+    ws = {}
+    for side, kind in (("post", post), ("pre", pre)):
+        w = normal(g, (N,), dtype) if kind != "none" and N != 64 else None
+        b = normal(g, (N,), dtype) if kind == "layer" else None
+        ws[side] = (kind, 1e-5, w, b)
+    say(f"[norm] {dtype} M={M} N={N} {post}/{pre} gate={gate}/{act} residual={rt}")
+    norms = {s: hts.Norm(k, w, b, e) for s, (k, e, w, b) in ws.items()}
+    xs, rs = strided(x, 8)[0], strided(r, 16)[0]
+    ro, robig = strided(torch.zeros_like(r), 24)
+    yo, yobig = strided(torch.zeros_like(x), 8)
+    got_r, got_y = hts.residual_norm(xs, rs, norms["post"], norms["pre"], gt, act, scale, residual_out=ro, out=yo)
+    arr = {s: (k, e, None if w is None else f64(w), None if b is None else f64(b)) for s, (k, e, w, b) in ws.items()}
+    wr, er, wy, ey = ref.residual_norm(f64(x), f64(r), arr["post"], arr["pre"], None if gt is None else f64(gt), act, scale)
+    assert np.all(np.abs(f64(got_r) - wr) <= ref.EPS[rt] / 2 * np.abs(wr) + er + ref.TINY[rt])
+    assert np.all(np.abs(f64(got_y) - wy) <= ref.EPS[dtype] / 2 * np.abs(wy) + ey + ref.TINY[dtype])
+    assert torch.all(robig[:, N:] == 7.0) and torch.all(yobig[:, N:] == 7.0)
+    # in place over the residual and the block's output: the same bits
+    r2, x2 = r.clone(), x.clone()
+    hts.residual_norm(x2, r2, norms["post"], norms["pre"], gt, act, scale, residual_out=r2, out=x2)
+    assert torch.equal(r2, got_r) and torch.equal(x2, got_y)
+
+
+def test_residual_norm_parts():
+    g = np.random.default_rng(3)
+    x, r = normal(g, (6, 512), "bf16"), normal(g, (6, 512), "f32")
+    n = hts.Norm("rms", normal(g, (512,), "bf16"), eps=1e-6)
+    # no block: the plain norm of the residual; nothing kept
+    keep, y = hts.residual_norm(None, r, pre=n, keep_residual=False, out_dtype=torch.bfloat16)
+    assert keep is None and y.dtype == torch.bfloat16
+    _, want = hts.residual_norm(torch.zeros_like(x), r, pre=n)
+    assert torch.equal(y, want)
+    # no residual: scale * block; no pre norm: no y
+    keep, y = hts.residual_norm(x, None, scale=2.0)
+    assert y is None and torch.equal(keep, x * 2)
+    # the gate of one row through a view of stride 0, and through a vector
+    gate = normal(g, (512,), "bf16")
+    a, _ = hts.residual_norm(x, r, gate=gate)
+    b, _ = hts.residual_norm(x, r, gate=gate.expand(6, 512))
+    assert torch.equal(a, b)
+    # y in place of the gate
+    full = normal(g, (6, 512), "bf16")
+    _, want = hts.residual_norm(x, r, pre=n, gate=full)
+    got = full.clone()
+    hts.residual_norm(x, r, pre=n, gate=got, out=got)
+    assert torch.equal(got, want)
+    # no rows
+    e, _ = hts.residual_norm(x[:0], r[:0], pre=n)
+    assert e.shape == (0, 512)
+
+
+def test_layer_norm_of_values_far_from_zero():
+    # mean 1000, deviation 1: a variance formed as E[x^2] - mean^2 in 32 bits would be off by percents
+    g = np.random.default_rng(4)
+    r = normal(g, (3, 4096), "f32") + 1000.0
+    _, y = hts.residual_norm(None, r, pre=hts.Norm("layer", eps=0.0), out_dtype=torch.float16)
+    _, _, want, e = ref.residual_norm(None, f64(r), ("none", 0, None, None), ("layer", 0.0, None, None), None, "none", 1.0)
+    assert np.all(np.abs(f64(y) - want) <= 2.0 ** -11 * np.abs(want) + e)
+    assert abs(float(f64(y).std()) - 1.0) < 1e-3
+
+
+def test_norm_keeps_nan_and_infinity_in_their_rows():
+    g = np.random.default_rng(5)
+    x, r = normal(g, (4, 256), "bf16"), normal(g, (4, 256), "bf16")
+    clean, cy = hts.residual_norm(x, r, pre=hts.Norm("rms"))
+    x[1, 3], x[2, 200] = float("nan"), float("inf")
+    kr, ky = hts.residual_norm(x, r, pre=hts.Norm("rms"))
+    for row in (0, 3):
+        assert torch.equal(kr[row], clean[row]) and torch.equal(ky[row], cy[row])
+    assert bool(torch.isnan(ky[1]).all()) and bool(torch.isnan(ky[2, 200])) and bool(torch.isinf(kr[2, 200]))
+
+
+# ---- refusals that need tensors on the GPU ---------------------------------
+
+def test_helpers_refuse():
+    q, c, table, width = _attn_case(128, 8, 2, 16, "token", "same", [20, 3], "bf16", 9)
+    t, n = i32(table)[:, :width], i32([20, 3])
+    plan = hts.rope_plan(128, device=DEV)
+    k = normal(np.random.default_rng(0), (2, 256), "bf16")
+    pos, slots = i32([0, 1]), torch.tensor([0, 1], device=DEV)
+    bad = [
+        lambda: hts.paged_attn(q[:, :128 * 7], c, t, n),                     # heads not a multiple of the cache's
+        lambda: hts.paged_attn(q.float(), c, t, n),
+        lambda: hts.paged_attn(q.half(), c, t, n),                           # another 16-bit type than the cache
+        lambda: hts.paged_attn(q, c, t, n[:1]),
+        lambda: hts.paged_attn(q, c, t.long(), n),
+        lambda: hts.paged_attn(q, c, t, n.long()),
+        lambda: hts.paged_attn(q, c, t, n.cpu()),
+        lambda: hts.paged_attn(q, c, t[:1], n),
+        lambda: hts.paged_attn(q, c, t, n, out=q[:, :512]),
+        lambda: hts.paged_attn(q, c, t, n, lse=torch.empty((2, 7), device=DEV)),
+        lambda: hts.paged_attn(q, c, t, n, window=-1),
+        lambda: hts.paged_attn(q.t().contiguous().t(), c, t, n),
+        lambda: hts.rope_cache(q, k, k, pos, slots.int(), plan, c),
+        lambda: hts.rope_cache(q, k, k[:1], pos, slots, plan, c),
+        lambda: hts.rope_cache(q, k[:, :128], k[:, :128], pos, slots, plan, c),
+        lambda: hts.rope_cache(q, k, k, pos.long(), slots, plan, c),
+        lambda: hts.rope(q, k.half(), pos, plan),
+        lambda: hts.rope(q, k, pos[:1], plan),
+        lambda: hts.KVCache(c.k, c.v.transpose(1, 2)),
+        lambda: hts.KVCache(c.k[:, :, :, ::2], c.v[:, :, :, ::2]),
+        lambda: hts.KVCache(c.k.expand(-1, -1, -1, -1)[:1].expand(4, -1, -1, -1), c.v[:1].expand(4, -1, -1, -1)),
+        lambda: hts.KVCache(c.k, c.v, k_scale=torch.ones(2, device=DEV)),
+        lambda: hts.kv_step(n, n, n, t, 16, -1),
+        lambda: hts.kv_step(n, n, n, t, 24, 4),
+        lambda: hts.kv_step(n, n.long(), n, t, 16, 4),
+        lambda: hts.kv_step(n, i32([1, 1]), i32([0]), t, 16, 4, free_head=n),
+        lambda: hts.residual_norm(q, q[:1]),
+        lambda: hts.residual_norm(q, q.half()),
+        lambda: hts.residual_norm(q, q, pre=hts.Norm("batch")),
+        lambda: hts.residual_norm(q, q, pre=hts.Norm("rms", torch.ones(8, device=DEV))),
+        lambda: hts.residual_norm(q, q, gate=q.float()),
+        lambda: hts.residual_norm(q[:, 1:], q[:, 1:]),
+        lambda: hts.residual_norm(q[:, :12], q[:, :12]),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(hts.HTSError):
+            f()
+            say(f"refusal {i} did not happen")

@@ -8,7 +8,9 @@ present, the calls raise.
 Low-level functions carry the C names (``hts_pack_plan``, ``hts_pack``,
 ``hts_unpack``, ``hts_gemm``, ``hts_dense_gemm``, ...); ``pack``, ``gemm``,
 ``unpack``, ``dense_gemm``, ``pack_masked``, ``wanda_tile_map`` and
-``wanda_global_maps`` are tensor-level helpers built on them.
+``wanda_global_maps`` are tensor-level helpers built on them.  The steps of a decoder block around its
+products (``kv_step``, ``rope``, ``rope_cache``, ``paged_attn``, ``residual_norm``) have theirs in
+``serving``, under this package's name too.
 """
 from __future__ import annotations
 
@@ -46,6 +48,30 @@ class hts_sizes(ctypes.Structure):
                 ("index_bytes", ctypes.c_uint64), ("n_sparse", ctypes.c_int64)]
 
 
+class hts_kv_desc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class hts_rope_scaling(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("rule", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("context", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
+
+
+class hts_rope_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rot", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class hts_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("r_dtype", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("pre", ctypes.c_int32), ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("gate_act", ctypes.c_int32)]
+
+
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -71,6 +97,20 @@ _SIGS = {
     "hts_col_norms": (ctypes.c_int, [_I32, _I64, _I64, _VP, _I64, _VP, _VP]),
     "hts_wanda_tile_cost": (ctypes.c_int, [ctypes.POINTER(hts_desc), _VP, _I64, _VP, _VP, _VP]),
     "hts_wanda_map": (ctypes.c_int, [_I64, _VP, _I64, _VP, _VP]),
+    "hts_kv_step": (ctypes.c_int, [_I64, _VP, _VP, _I32, _VP, _I64, _VP, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP,
+                                   _VP, _VP]),
+    "hts_rope_plan": (ctypes.c_int, [ctypes.POINTER(hts_rope_scaling), _VP]),
+    "hts_rope": (ctypes.c_int, [ctypes.POINTER(hts_rope_desc), _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I64, _VP,
+                                _I64, _VP]),
+    "hts_rope_cache": (ctypes.c_int, [ctypes.POINTER(hts_rope_desc), _VP, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP,
+                                      _I64, _VP, _I64, ctypes.POINTER(hts_kv_desc), _VP, _VP, _VP, _VP, _VP]),
+    "hts_paged_attn": (ctypes.c_int, [_I32, _I64, _I32, ctypes.POINTER(hts_kv_desc), _VP, _I64, _VP, _VP, _VP, _VP,
+                                      _VP, _I64, _I64, _VP, ctypes.c_float, _I64, _VP, _I64, _VP, _VP,
+                                      ctypes.c_size_t, _VP]),
+    "hts_paged_attn_workspace": (ctypes.c_int, [_I64, _I32, ctypes.POINTER(hts_kv_desc), _I64, _I64,
+                                                ctypes.POINTER(ctypes.c_size_t)]),
+    "hts_residual_norm": (ctypes.c_int, [ctypes.POINTER(hts_norm_desc), _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I64,
+                                         _VP, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -113,6 +153,11 @@ def _torch_dt(code: int):
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _ld(t: Optional[torch.Tensor]) -> int:
+    """Leading dimension: elements between rows (0: no matrix, or one row shared by all)."""
+    return t.stride(0) if t is not None and t.dim() == 2 else 0
 
 
 def _stream(stream) -> Optional[int]:
@@ -241,6 +286,57 @@ def hts_wanda_tile_cost(desc, W, col_scale, cost, stream=None) -> None:
 
 def hts_wanda_map(cost, n_sparse: int, tile_map, stream=None) -> None:
     _check(lib().hts_wanda_map(cost.numel(), _ptr(cost), n_sparse, _ptr(tile_map), _stream(stream)))
+
+
+def hts_kv_step(cached, added, page: int, free_pages, free_head, block_table, lengths, starts, slots, positions,
+                head_out, stream=None) -> None:
+    _check(lib().hts_kv_step(cached.numel(), _ptr(cached), _ptr(added), page, _ptr(free_pages), free_pages.numel(),
+                             _ptr(free_head), _ptr(block_table), block_table.stride(0), block_table.shape[1],
+                             slots.numel(), _ptr(lengths), _ptr(starts), _ptr(slots), _ptr(positions), _ptr(head_out),
+                             _stream(stream)))
+
+
+def hts_rope_plan(scaling: hts_rope_scaling) -> np.ndarray:
+    """Host-side plan: turns per position of each pair, float64[rot/2] numpy."""
+    turns = np.zeros(max(scaling.rot // 2, 1), dtype=np.float64)
+    _check(lib().hts_rope_plan(ctypes.byref(scaling), turns.ctypes.data))
+    return turns
+
+
+def hts_rope(desc: hts_rope_desc, turns, positions, Q, Q_out, K, K_out, stream=None) -> None:
+    _check(lib().hts_rope(ctypes.byref(desc), _ptr(turns), positions.numel(), _ptr(positions),
+                          _ptr(Q), _ld(Q), _ptr(Q_out), _ld(Q_out), _ptr(K), _ld(K), _ptr(K_out), _ld(K_out),
+                          _stream(stream)))
+
+
+def hts_rope_cache(desc: hts_rope_desc, turns, positions, slots, Q, Q_out, K, V, kv: hts_kv_desc, k_cache, v_cache,
+                   k_scale=None, v_scale=None, stream=None) -> None:
+    _check(lib().hts_rope_cache(ctypes.byref(desc), _ptr(turns), positions.numel(), _ptr(positions), _ptr(slots),
+                                _ptr(Q), _ld(Q), _ptr(Q_out), _ld(Q_out), _ptr(K), _ld(K), _ptr(V), _ld(V),
+                                ctypes.byref(kv), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                _stream(stream)))
+
+
+def hts_paged_attn_workspace(B: int, q_heads: int, kv: hts_kv_desc, width: int, window: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hts_paged_attn_workspace(B, q_heads, ctypes.byref(kv), width, window, ctypes.byref(n)))
+    return n.value
+
+
+def hts_paged_attn(q_heads: int, kv: hts_kv_desc, Q, k_cache, v_cache, block_table, lengths, scale: float, O,
+                   k_scale=None, v_scale=None, window: int = 0, lse=None, workspace=None, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().hts_paged_attn(_dt(Q.dtype), Q.shape[0], q_heads, ctypes.byref(kv), _ptr(Q), Q.stride(0),
+                                _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                                block_table.stride(0), block_table.shape[1], _ptr(lengths), scale, window, _ptr(O),
+                                O.stride(0), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def hts_residual_norm(desc: hts_norm_desc, M: int, N: int, block, post_weight, post_bias, gate, R, pre_weight,
+                      pre_bias, R_out, Y, stream=None) -> None:
+    _check(lib().hts_residual_norm(ctypes.byref(desc), M, N, _ptr(block), _ld(block), _ptr(post_weight),
+                                   _ptr(post_bias), _ptr(gate), _ld(gate), _ptr(R), _ld(R), _ptr(pre_weight),
+                                   _ptr(pre_bias), _ptr(R_out), _ld(R_out), _ptr(Y), _ld(Y), _stream(stream)))
 
 
 # --------------------------------------------------------------------------
@@ -439,3 +535,7 @@ def bits_from_tensor(t: torch.Tensor) -> np.ndarray:
     if t.dtype in (torch.float8_e4m3fn, torch.uint8):
         return t.detach().contiguous().view(torch.uint8).cpu().numpy()
     return t.detach().contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+from .serving import (KVCache, KVStep, Norm, RopePlan, kv_cache, kv_step, paged_attn, residual_norm, rope,  # noqa: E402
+                      rope_cache, rope_plan)

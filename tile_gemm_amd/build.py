@@ -20,7 +20,8 @@ PEAK_LIB = os.path.join(PKG, "libhts_peak.so")
 PEAK_SOURCES = ["peak.hip"]
 OBJDIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["hts_api.cpp", "pack.hip", "gemm_decode.hip", "gemm_prefill.hip", "wanda.hip", "elementwise.hip"]
+SOURCES = ["hts_api.cpp", "pack.hip", "gemm_decode.hip", "gemm_prefill.hip", "wanda.hip", "elementwise.hip",
+           "serve_api.cpp", "kv_step.hip", "rope.hip", "attn_decode.hip", "norm.hip"]
 
 ARCH = "gfx950"
 COMMON = [

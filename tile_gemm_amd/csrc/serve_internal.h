@@ -1,0 +1,86 @@
+// Internal declarations shared by the serving half of the C API and its gfx950 kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "hts.h"
+
+namespace hts {
+
+// hts_kv_step keeps one prefix-sum entry of each kind per request in LDS.
+constexpr int kMaxStepRequests = 4096;
+struct KvStepArgs {
+    int32_t B;
+    int32_t page_shift;
+    const int32_t *cached, *added;
+    const int32_t* free_pages;
+    int64_t n_free;
+    const int32_t* free_head;
+    int32_t* table;
+    int64_t ldt, width, tokens;
+    int32_t *lengths, *starts;
+    int64_t* slots;
+    int32_t *positions, *head_out;
+};
+hipError_t launch_kv_step(const KvStepArgs& a, hipStream_t s);
+
+struct RopeArgs {
+    int32_t dtype, layout, dim, rot, q_heads, k_heads;
+    float magnitude;
+    int64_t T;
+    const double* turns;
+    const int32_t* positions;
+    const uint16_t *Q, *K, *V;
+    uint16_t *Qo, *Ko;         // Ko: nullptr where K goes to the cache
+    int64_t ldq, ldqo, ldk, ldko, ldv;
+    const int64_t* slots;      // nullptr: no cache
+    void *kc, *vc;
+    const float *k_scale, *v_scale;
+    int64_t n_slots;
+    int32_t cache8, page_shift;
+    int64_t page_stride, token_stride, head_stride;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+
+struct AttnArgs {
+    int32_t dtype, cache8;
+    int32_t B, q_heads, k_heads, dim, page_shift;
+    int64_t pages, page_stride, token_stride, head_stride;
+    const uint16_t* Q;
+    int64_t ldq;
+    const void *kc, *vc;
+    const float *k_scale, *v_scale;
+    const int32_t* table;
+    int64_t ldt, width;
+    const int32_t* lengths;
+    float scale;
+    int64_t window;            // 0: none
+    uint16_t* O;
+    int64_t ldo;
+    float* lse;
+};
+hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
+
+constexpr int64_t kMaxNormWidth = 32768;
+struct NormArgs {
+    int32_t dtype, r32, post, pre, gate_act;
+    float post_eps, pre_eps, scale;
+    int64_t M;
+    int32_t N;
+    const uint16_t* block;
+    int64_t ldb;
+    const uint16_t *post_w, *post_b;
+    const uint16_t* gate;
+    int64_t ldg;
+    const void* R;
+    int64_t ldr;
+    const uint16_t *pre_w, *pre_b;
+    void* R_out;
+    int64_t ldro;
+    uint16_t* Y;
+    int64_t ldy;
+};
+hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s);
+
+}  // namespace hts
