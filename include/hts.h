@@ -291,7 +291,8 @@ hts_status hts_wanda_map(int64_t T, const double* cost, int64_t n_sparse, uint8_
  * `dim` values.  Element (p, t, h, d) of K (and, with the same strides, of V) is at
  * p*page_stride + t*token_stride + h*head_stride + d, in elements.  page: a power of two, 16 to
  * 1024.  dim: a multiple of 8, 8 to 256.  Strides: multiples of 8, with no two elements at one
- * place (any nesting of pages, tokens and heads; the stride of an axis of size 1 is not used).
+ * place (any nesting of pages, tokens and heads; the stride of an axis of size 1 is not used) and
+ * token_stride below 2^26.
  * dtype: HTS_F16, HTS_BF16 or HTS_FP8_E4M3; an 8-bit cache holds value / scale, with one float
  * scale per head (k_scale, v_scale; NULL = 1), which must be positive and finite. */
 typedef struct {
@@ -333,7 +334,7 @@ hts_status hts_kv_step(int64_t B, const int32_t* cached, const int32_t* added, i
 enum { HTS_ROPE_HALF = 0, HTS_ROPE_INTERLEAVED = 1 };
 
 /* f_i = theta^(-2i/rot), i < rot/2, scaled for contexts longer than the trained one by `factor`:
- *   HTS_ROPE_PLAIN      : f_i (factor must be 1)
+ *   HTS_ROPE_PLAIN      : f_i (factor is not used)
  *   HTS_ROPE_LINEAR     : f_i / factor
  *   HTS_ROPE_BASE       : theta * factor^(rot / (rot - 2)) in place of theta
  *   HTS_ROPE_RAMP       : f_i * (c + (1 - c) / factor), c = (n_i - low) / (high - low) clamped to

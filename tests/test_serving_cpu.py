@@ -112,7 +112,7 @@ def test_cache_descriptions_that_are_taken():
         assert hts.lib().hts_paged_attn_workspace(4, 32, by(kv(**change)), 8, 0, by(n)) == 0, change
 
 
-@pytest.mark.parametrize("rule,factor,context", [("plain", 1.0, 0.0), ("linear", 4.0, 0.0), ("base", 8.0, 0.0),
+@pytest.mark.parametrize("rule,factor,context", [("plain", 1.0, 0.0), ("plain", 3.0, 0.0), ("linear", 4.0, 0.0), ("base", 8.0, 0.0),
                                                  ("ramp", 8.0, 4096.0), ("ramp_pairs", 16.0, 4096.0),
                                                  ("ramp_pairs", 2.5, 100.0)])
 @pytest.mark.parametrize("rot", [8, 64, 128, 256])
@@ -134,7 +134,7 @@ def test_rope_plan_refuses():
     assert plan() == 0
     assert plan(rot=0) == 7 and plan(rot=12) == 7 and plan(rot=264) == 7
     for bad in (dict(rule=5), dict(rule=-1), dict(theta=1.0), dict(theta=float("nan")), dict(factor=0.5),
-                dict(factor=2.0), dict(rule=1, factor=float("inf")), dict(rule=3, factor=2.0, context=0.0),
+                dict(rule=1, factor=float("inf")), dict(rule=3, factor=2.0, context=0.0),
                 dict(rule=3, factor=2.0, low=0.0), dict(rule=4, factor=2.0, high=1.0),
                 dict(rule=2, rot=8, theta=1e300, factor=1e300)):
         assert plan(**bad) == 1, bad

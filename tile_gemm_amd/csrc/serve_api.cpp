@@ -60,6 +60,8 @@ hts_status check_kv(const hts_kv_desc* kv, int32_t dtype, const float* k_scale, 
                {kv->heads, kv->head_stride, "head_stride"}};
     for (auto& x : ax) {
         if (x.n == 1) x.stride = int64_t(1) << 61;   // not used; sorts last
+        else if (&x == &ax[1] && x.stride >= (int64_t(1) << 26))
+            return fail(HTS_ERR_UNSUPPORTED, "token_stride=%lld is not below 2^26", (long long)x.stride);
         else if (x.stride <= 0 || x.stride >= (int64_t(1) << 48))
             return fail(HTS_ERR_SHAPE, "%s=%lld is not positive (below 2^48)", x.name, (long long)x.stride);
         else if (x.stride % 8)
@@ -90,6 +92,35 @@ hts_status check_table(const int32_t* table, int64_t B, int64_t ldt, int64_t wid
     if (ldt < width || ldt >= kInt32)
         return fail(HTS_ERR_SHAPE, "ldt=%lld is not from width=%lld to 2^31 - 1", (long long)ldt, (long long)width);
     return B ? check_aligned(table, 4, "block_table") : HTS_OK;
+}
+
+// How hts_paged_attn divides its work.  Workgroups in all: 4 to a CU (they hold 3 or 4 there), divided by the
+// cache heads and head tiles, each of which takes all requests.
+struct AttnPlan {
+    int32_t head_tiles, tile_heads, target;
+    uint32_t cap, window, min_chunk;
+    bool split;
+    uint64_t plan_bytes, ml_bytes, bytes;
+};
+AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t width, int64_t window) {
+    AttnPlan p{};
+    const int32_t group = q_heads / kv->heads;
+    p.head_tiles = (group + 15) / 16;
+    p.tile_heads = std::min(group, 16);
+    p.cap = (uint32_t)std::min<int64_t>(width * kv->page, kInt32 - 1);
+    p.window = (uint32_t)std::min<int64_t>(window, kInt32 - 1);
+    p.min_chunk = 256;
+    const int64_t rows = (int64_t)kv->heads * p.head_tiles;
+    p.target = (int32_t)((1024 + rows - 1) / rows);
+    const uint64_t most = window ? std::min<uint64_t>(p.cap, (uint64_t)p.window + 31) : p.cap;
+    p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > p.min_chunk;
+    if (p.split) {
+        const uint64_t parts = 2 * (uint64_t)p.target * rows * p.tile_heads;
+        p.plan_bytes = (8 * (uint64_t)B + 255) & ~uint64_t(255);
+        p.ml_bytes = (8 * parts + 255) & ~uint64_t(255);
+        p.bytes = p.plan_bytes + p.ml_bytes + 4 * parts * kv->dim;
+    }
+    return p;
 }
 
 hts_status check_rope(const hts_rope_desc* d, const double* turns, int64_t T, const int32_t* positions) {
@@ -210,8 +241,6 @@ hts_status hts_rope_plan(const hts_rope_scaling* s, double* turns_host) {
         return fail(HTS_ERR_INVALID_ARG, "rule %d is not a scaling rule", s->rule);
     if (!(std::isfinite(s->theta) && s->theta > 1.0)) return fail(HTS_ERR_INVALID_ARG, "theta must be above 1");
     if (!(std::isfinite(s->factor) && s->factor >= 1.0)) return fail(HTS_ERR_INVALID_ARG, "factor must be at least 1");
-    if (s->rule == HTS_ROPE_PLAIN && s->factor != 1.0)
-        return fail(HTS_ERR_INVALID_ARG, "plain frequencies take factor 1");
     const bool ramp = s->rule == HTS_ROPE_RAMP || s->rule == HTS_ROPE_RAMP_PAIRS;
     if (ramp && !(std::isfinite(s->context) && s->context > 0.0 && s->low > 0.0 && s->high > s->low && std::isfinite(s->high)))
         return fail(HTS_ERR_INVALID_ARG, "a ramp takes context > 0 and 0 < low < high");
@@ -336,7 +365,7 @@ hts_status hts_paged_attn_workspace(int64_t B, int32_t q_heads, const hts_kv_des
         return fail(HTS_ERR_SHAPE, "q_heads=%d is not a multiple of the cache's %d heads (up to 65535)", q_heads, kv->heads);
     if (width < 1 || width >= kInt32) return fail(HTS_ERR_SHAPE, "width=%lld is not from 1 to 2^31 - 1", (long long)width);
     if (window < 0) return fail(HTS_ERR_SHAPE, "window=%lld is negative", (long long)window);
-    *bytes = 0;
+    *bytes = (size_t)attn_plan(B, q_heads, kv, width, window).bytes;
     return ok();
 }
 
@@ -354,6 +383,8 @@ hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_k
     if (!std::isfinite(scale)) return fail(HTS_ERR_INVALID_ARG, "scale is not finite");
     if (window < 0) return fail(HTS_ERR_SHAPE, "window=%lld is negative", (long long)window);
     const int64_t n = (int64_t)q_heads * kv->dim;
+    if ((int64_t)kv->heads * ((q_heads / kv->heads + 15) / 16) > 65535)
+        return fail(HTS_ERR_UNSUPPORTED, "cache heads times tiles of 16 query heads exceed 65535");
     if ((st = check_table(block_table, B, ldt, width)) || (st = check_ld(ldq, n, 8, "ldq")) ||
         (st = check_ld(ldo, n, 8, "ldo")))
         return st;
@@ -398,10 +429,22 @@ hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_k
     a.width = width;
     a.lengths = lengths;
     a.scale = scale;
-    a.window = window;
     a.O = static_cast<uint16_t*>(O);
     a.ldo = ldo;
     a.lse = lse;
+    const AttnPlan p = attn_plan(B, q_heads, kv, width, window);
+    a.window = p.window;
+    a.cap = p.cap;
+    a.head_tiles = p.head_tiles;
+    a.tile_heads = p.tile_heads;
+    a.target = p.target;
+    a.min_chunk = p.min_chunk;
+    if (p.split && workspace && workspace_bytes >= p.bytes) {
+        char* ws = static_cast<char*>(workspace);
+        a.plan = reinterpret_cast<uint2*>(ws);
+        a.part_ml = reinterpret_cast<float2*>(ws + p.plan_bytes);
+        a.part_o = reinterpret_cast<float*>(ws + p.plan_bytes + p.ml_bytes);
+    }
     return hip_status(hts::launch_attn(a, static_cast<hipStream_t>(stream)), "attention kernel launch");
 }
 

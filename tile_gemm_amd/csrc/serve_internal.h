@@ -55,11 +55,23 @@ struct AttnArgs {
     int64_t ldt, width;
     const int32_t* lengths;
     float scale;
-    int64_t window;            // 0: none
+    uint32_t window;           // 0: none
+    uint32_t cap;              // tokens a row of the table holds
     uint16_t* O;
     int64_t ldo;
     float* lse;
+    int32_t head_tiles, tile_heads;   // tiles of 16 query heads to a cache head; heads of a tile (<= 16)
+    // Split over the length (part_o not NULL): chunks of total / target tokens, at least min_chunk, in at
+    // most 2 * target parts of split requests (a request of e tokens in chunks of c > total / target has
+    // ceil(e / c) <= 2 e / c of them, where it has more than one).
+    int32_t target;
+    uint32_t min_chunk;
+    uint2* plan;               // [B]: first part, number of chunks
+    float2* part_ml;           // [2 target][k_heads * head_tiles][tile_heads]
+    float* part_o;             // the same, [dim]
 };
+// Requests whose division every wave can find in one pass; more run unsplit.
+constexpr int64_t kMaxSplitRequests = 4096;
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
 constexpr int64_t kMaxNormWidth = 32768;
