@@ -39,56 +39,74 @@ def _choice(table: dict, key, what: str) -> int:
     return table[key]
 
 
-def _here(device: torch.device, **tensors) -> None:
-    """Every tensor given lives on this GPU."""
-    if device.type != "cuda":
-        _bad(f"tensors must be on a GPU, not on {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            _bad(f"{name} is on {t.device}, the other tensors on {device}")
-
-
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtypes) -> None:
+def _explain(t, name: str, rows, cols, dtypes, dev: int):
+    """Say what is wrong with a tensor that a check below has refused."""
+    if t.get_device() != dev:
+        _bad(f"{name} is on {t.device}, expected GPU {dev}" if dev >= 0 else f"{name} must be on a GPU, not on {t.device}")
     if t.dtype not in dtypes:
         _bad(f"{name} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}", 2)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        _bad(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}", 3)
-    if rows and cols > 1 and t.stride(1) != 1:
-        _bad(f"the rows of {name} must be contiguous", 3)
+    want = (rows,) if cols is None else (rows, cols)
+    if tuple(t.shape) != want:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {want}", 3)
+    _bad(f"{name} must be contiguous along its rows", 3)
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype) -> None:
-    if t.dtype != dtype:
-        _bad(f"{name} has type {t.dtype}, expected {dtype}", 2)
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        _bad(f"{name} must be a contiguous vector of {n} entries", 3)
+def _gpu(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _bad(f"{name} must be on a GPU, not on {t.device}")
+    return dev
+
+
+def _lead(t: torch.Tensor, name: str, rows: int, cols: int, dtype, dev: int) -> int:
+    """Leading dimension of a [rows, cols] matrix of this type on this GPU (a matrix of one row may carry any
+    stride there: it gets one that the library takes)."""
+    if t.dtype is dtype and t.get_device() == dev and t.dim() == 2:
+        r, c = t.shape
+        if r == rows and c == cols:
+            lead, one = t.stride()
+            if one == 1 or cols <= 1 or rows == 0:
+                return lead if rows > 1 else (cols + 7) // 8 * 8
+    return _explain(t, name, rows, cols, (dtype,), dev)
+
+
+def _vec(t: torch.Tensor, name: str, n: int, dtype, dev: int) -> int:
+    """Address of a contiguous vector of n entries of this type on this GPU."""
+    if t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.shape[0] == n and (n <= 1 or t.stride(0) == 1):
+        return t.data_ptr()
+    return _explain(t, name, n, None, (dtype,), dev)
+
+
+def _table(t: torch.Tensor, rows: int, dev: int) -> int:
+    """Leading dimension of a block table int32 [rows, width]."""
+    if t.dim() != 2:
+        _bad("block_table must be [requests, pages of a request]", 3)
+    width = t.shape[1]
+    _lead(t, "block_table", rows, width, torch.int32, dev)
+    return t.stride(0) if rows > 1 else width
 
 
 @contextlib.contextmanager
-def _switched(device, stream):
-    with torch.cuda.device(device):
+def _switched(dev, stream):
+    with torch.cuda.device(dev):
         if stream is None:
             yield
         else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-            if s.device != device:
-                _bad(f"the stream belongs to {s.device}, the tensors to {device}")
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
+            if s.device_index != dev:
+                _bad(f"the stream belongs to GPU {s.device_index}, the tensors to GPU {dev}")
             with torch.cuda.stream(s):
                 yield
 
 
-def _scope(device: torch.device, stream):
+_STAY = contextlib.nullcontext()
+
+
+def _scope(dev: int, stream):
     """Make the tensors' GPU and the call's stream current, for the launch and for what it allocates."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return _switched(device, stream)
-
-
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """The matrix with a leading dimension the library takes: a matrix of one row may carry any."""
-    if t.dim() == 2 and t.shape[0] <= 1 and t.shape[1] and (t.stride(0) < t.shape[1] or t.stride(0) % 8):
-        return t.as_strided(t.shape, ((t.shape[1] + 7) // 8 * 8, 1))
-    return t
+    if stream is None and torch.cuda.current_device() == dev:
+        return _STAY
+    return _switched(dev, stream)
 
 
 # --------------------------------------------------------------------------
@@ -109,19 +127,34 @@ class KVCache:
         used = [i for i in range(3) if k.shape[i] > 1]
         if any(k.stride(i) != v.stride(i) for i in used) or k.stride(3) != 1 or v.stride(3) != 1:
             _bad("k and v must have one set of strides, with the entries of a head consecutive", 3)
-        _here(k.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        dev = _gpu(k, "k")
+        if v.get_device() != dev:
+            _bad(f"v is on {v.device}, k on {k.device}")
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
             if s is not None:
-                _vector(s, name, k.shape[2], torch.float32)
+                _vec(s, name, k.shape[2], torch.float32, dev)
                 if k.dtype != torch.float8_e4m3fn:
                     _bad(f"{name} belongs to an 8-bit cache")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.gpu, self.dtype = k.device, dev, k.dtype
         self.pages, self.page, self.heads, self.dim = k.shape
         self.desc = _c.hts_kv_desc(self.pages, self.page, self.heads, self.dim, _c._dt(k.dtype), k.stride(0),
                                    k.stride(1), k.stride(2))
         # the descriptor's checks, once, before any step uses it
         _c.hts_paged_attn_workspace(0, self.heads, self.desc, 1)
+        self._desc = ctypes.byref(self.desc)
+        self._workspace = {}     # bytes by (requests, heads, width, window)
+
+    def workspace_bytes(self, requests: int, q_heads: int, width: int, window: int = 0) -> int:
+        """Bytes hts_paged_attn takes to split these sizes over their length."""
+        key = (requests, q_heads, width, window)
+        got = self._workspace.get(key)
+        if got is None:
+            got = _c.hts_paged_attn_workspace(requests, q_heads, self.desc, width, window)
+            if len(self._workspace) > 1000:
+                self._workspace.clear()
+            self._workspace[key] = got
+        return got
 
 
 def kv_cache(pages: int, page: int, heads: int, dim: int, dtype, device="cuda", order: str = "token",
@@ -149,10 +182,11 @@ class KVStep:
 
     @staticmethod
     def buffers(requests: int, tokens: int, device) -> "KVStep":
-        i32 = dict(dtype=torch.int32, device=device)
-        return KVStep(torch.empty(requests, **i32), torch.empty(requests + 1, **i32),
-                      torch.empty(tokens, dtype=torch.int64, device=device), torch.empty(tokens, **i32),
-                      torch.empty(1, **i32))
+        """Buffers for a step, in one allocation."""
+        sizes = (2 * tokens, tokens, requests, requests + 1, 1)
+        slots, positions, lengths, starts, head = torch.empty(
+            3 * tokens + 2 * requests + 2, dtype=torch.int32, device=device).split_with_sizes(sizes)
+        return KVStep(lengths, starts, slots.view(torch.int64), positions, head)
 
 
 def kv_step(cached: torch.Tensor, added: torch.Tensor, free_pages: torch.Tensor, block_table: torch.Tensor,
@@ -162,32 +196,26 @@ def kv_step(cached: torch.Tensor, added: torch.Tensor, free_pages: torch.Tensor,
     block_table (int32 [B, width], in place) gains the pages the new tokens open, taken from free_pages in
     order from entry free_head on.  ``tokens`` is the step's capacity: tokens past the batch's last one get
     slot and position -1.  Where head ends above free_pages.numel() the list was too short."""
-    dev, B = cached.device, cached.numel()
-    _here(dev, added=added, free_pages=free_pages, block_table=block_table, free_head=free_head)
-    _vector(cached, "cached", B, torch.int32)
-    _vector(added, "added", B, torch.int32)
-    _vector(free_pages, "free_pages", free_pages.numel(), torch.int32)
-    if block_table.dim() != 2:
-        _bad("block_table must be [requests, pages of a request]", 3)
-    _matrix(block_table, "block_table", B, block_table.shape[1], (torch.int32,))
+    dev, B, i32 = _gpu(cached, "cached"), cached.numel(), torch.int32
+    at_cached, at_added = _vec(cached, "cached", B, i32, dev), _vec(added, "added", B, i32, dev)
+    n_free = free_pages.numel()
+    at_free = _vec(free_pages, "free_pages", n_free, i32, dev)
+    at_head = None if free_head is None else _vec(free_head, "free_head", 1, i32, dev)
+    ldt = _table(block_table, B, dev)
     if tokens < 0:
         _bad(f"tokens={tokens} is negative", 3)
-    if free_head is not None:
-        _vector(free_head, "free_head", 1, torch.int32)
+    if out is not None:
+        for t, name, n in ((out.lengths, "lengths", B), (out.starts, "starts", B + 1),
+                           (out.positions, "positions", tokens), (out.head, "head", 1)):
+            _vec(t, name, n, i32, dev)
+        _vec(out.slots, "slots", tokens, torch.int64, dev)
     with _scope(dev, stream):
         if out is None:
-            out = KVStep.buffers(B, tokens, dev)
-        else:
-            _here(dev, lengths=out.lengths, starts=out.starts, slots=out.slots, positions=out.positions, head=out.head)
-            _vector(out.lengths, "lengths", B, torch.int32)
-            _vector(out.starts, "starts", B + 1, torch.int32)
-            _vector(out.slots, "slots", tokens, torch.int64)
-            _vector(out.positions, "positions", tokens, torch.int32)
-            _vector(out.head, "head", 1, torch.int32)
-        if B <= 1 and block_table.stride(0) < block_table.shape[1]:
-            block_table = block_table.as_strided(block_table.shape, (block_table.shape[1], 1))
-        _c.hts_kv_step(cached, added, page, free_pages, free_head, block_table, out.lengths, out.starts, out.slots,
-                       out.positions, out.head)
+            out = KVStep.buffers(B, tokens, cached.device)
+        _c._check(_c.lib().hts_kv_step(
+            B, at_cached, at_added, page, at_free, n_free, at_head, block_table.data_ptr(), ldt, block_table.shape[1],
+            tokens, out.lengths.data_ptr(), out.starts.data_ptr(), out.slots.data_ptr(), out.positions.data_ptr(),
+            out.head.data_ptr(), _c._current_stream(dev)))
     return out
 
 
@@ -220,39 +248,51 @@ def rope_plan(dim: int, rot: Optional[int] = None, theta: float = 10000.0, layou
     return RopePlan(torch.from_numpy(turns).to(device), lay, dim, rot, magnitude)
 
 
-def _rope_checks(q, k, positions, plan, q_out, k_out):
-    ref = q if q is not None else k
-    if ref is None:
-        _bad("q and k are both missing")
-    T, dev = positions.numel(), ref.device
-    _here(dev, q=q, k=k, q_out=q_out, k_out=k_out, positions=positions, turns=plan.turns)
-    _vector(positions, "positions", T, torch.int32)
-    heads = []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            heads.append(0)
-            continue
-        if x.dim() != 2 or x.shape[1] % plan.dim:
-            _bad(f"{name} must be [tokens, heads * {plan.dim}]", 3)
-        _matrix(x, name, T, x.shape[1], _16)
-        if x.dtype != ref.dtype:
-            _bad("q and k must share a type", 2)
-        if out is not None:
-            _matrix(out, name + "_out", T, x.shape[1], (x.dtype,))
-        heads.append(x.shape[1] // plan.dim)
-    return dev, heads, _c.hts_rope_desc(_c._dt(ref.dtype), plan.layout, plan.dim, plan.rot, heads[0], heads[1],
-                                        plan.magnitude, 0)
+_rope_descs = {}
+
+
+def _rope_desc(dtype, plan: RopePlan, q_heads: int, k_heads: int):
+    key = (dtype, plan.layout, plan.dim, plan.rot, q_heads, k_heads, plan.magnitude)
+    got = _rope_descs.get(key)
+    if got is None:
+        if len(_rope_descs) > 1000:
+            _rope_descs.clear()
+        d = _c.hts_rope_desc(_c._dt(dtype), plan.layout, plan.dim, plan.rot, q_heads, k_heads, plan.magnitude, 0)
+        got = _rope_descs[key] = ctypes.byref(d)
+    return got
+
+
+def _rope_heads(x: torch.Tensor, name: str, dim: int) -> int:
+    if x.dim() != 2 or x.shape[1] % dim:
+        _bad(f"{name} must be [tokens, heads * {dim}]", 3)
+    if x.dtype not in _16:
+        _bad(f"{name} has type {x.dtype}, expected float16 or bfloat16", 2)
+    return x.shape[1] // dim
 
 
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, plan: RopePlan,
          q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
     """Rotate q and k (either may be None) by their rows' positions (int32[T]), into q_out and k_out, or in
     place where none is given.  Rows with a negative position are left as they were.  Returns (q_out, k_out)."""
-    dev, _, desc = _rope_checks(q, k, positions, plan, q_out, k_out)
+    ref = q if q is not None else k
+    if ref is None:
+        _bad("q and k are both missing")
+    dev, T = _gpu(ref, "q" if ref is q else "k"), positions.numel()
+    at = _vec(positions, "positions", T, torch.int32, dev)
+    turns = _vec(plan.turns, "plan", plan.rot // 2, torch.float64, dev)
     q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    heads, args = [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            heads.append(0)
+            args += (None, 0, None, 0)
+            continue
+        heads.append(_rope_heads(x, name, plan.dim))
+        n = x.shape[1]
+        args += (x.data_ptr(), _lead(x, name, T, n, ref.dtype, dev),
+                 out.data_ptr(), _lead(out, name + "_out", T, n, ref.dtype, dev))
     with _scope(dev, stream):
-        r = [None if x is None else _rows(x) for x in (q, q_out, k, k_out)]
-        _c.hts_rope(desc, plan.turns, positions, *r)
+        _c._check(_c.lib().hts_rope(_rope_desc(ref.dtype, plan, *heads), turns, T, at, *args, _c._current_stream(dev)))
     return q_out, k_out
 
 
@@ -261,15 +301,21 @@ def rope_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
     """Rotate q (into q_out, or in place) and write the rotated k, and v, of token t to slot slots[t] (int64)
     of the cache.  Tokens with a negative position are skipped; tokens with a slot outside the cache are not
     cached.  Slots must differ from one another.  Returns q_out."""
-    dev, heads, desc = _rope_checks(q, k, positions, plan, q_out, None)
-    _here(dev, v=v, slots=slots, k_cache=cache.k)
-    T = positions.numel()
-    _matrix(v, "v", T, k.shape[1], (k.dtype,))
-    _vector(slots, "slots", T, torch.int64)
+    dev, T, dt, dim = _gpu(q, "q"), positions.numel(), q.dtype, plan.dim
+    if cache.gpu != dev:
+        _bad(f"the cache is on GPU {cache.gpu}, q on GPU {dev}")
+    hq, hk = _rope_heads(q, "q", dim), _rope_heads(k, "k", dim)
+    nq, nk = hq * dim, hk * dim
     q_out = q if q_out is None else q_out
+    ks, vs = cache.k_scale, cache.v_scale
+    args = (_rope_desc(dt, plan, hq, hk), _vec(plan.turns, "plan", plan.rot // 2, torch.float64, dev), T,
+            _vec(positions, "positions", T, torch.int32, dev), _vec(slots, "slots", T, torch.int64, dev),
+            q.data_ptr(), _lead(q, "q", T, nq, dt, dev), q_out.data_ptr(), _lead(q_out, "q_out", T, nq, dt, dev),
+            k.data_ptr(), _lead(k, "k", T, nk, dt, dev), v.data_ptr(), _lead(v, "v", T, nk, dt, dev), cache._desc,
+            cache.k.data_ptr(), cache.v.data_ptr(), None if ks is None else ks.data_ptr(),
+            None if vs is None else vs.data_ptr())
     with _scope(dev, stream):
-        _c.hts_rope_cache(desc, plan.turns, positions, slots, _rows(q), _rows(q_out), _rows(k), _rows(v), cache.desc,
-                          cache.k, cache.v, cache.k_scale, cache.v_scale)
+        _c._check(_c.lib().hts_rope_cache(*args, _c._current_stream(dev)))
     return q_out
 
 
@@ -285,36 +331,38 @@ def paged_attn(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lengt
     b in the cache (its pages in block_table, int32 [B, width]), or over the last ``window`` of them.
     scale: default 1 / sqrt(head size).  lse (float32 [B, q heads]) receives the logarithm of the softmax's
     sum.  A request without tokens gets zeros.  The workspace is allocated here when none is given."""
-    dev, B = q.device, q.shape[0]
-    _here(dev, k_cache=cache.k, block_table=block_table, lengths=lengths, out=out, lse=lse, workspace=workspace)
+    dev, dt = _gpu(q, "q"), q.dtype
+    if cache.gpu != dev:
+        _bad(f"the cache is on GPU {cache.gpu}, q on GPU {dev}")
     if q.dim() != 2 or not q.shape[1] or q.shape[1] % (cache.dim * cache.heads):
         _bad(f"q must be [requests, heads * {cache.dim}], its heads a multiple of the cache's {cache.heads}", 3)
-    _matrix(q, "q", B, q.shape[1], _16)
-    heads = q.shape[1] // cache.dim
-    if block_table.dim() != 2:
-        _bad("block_table must be [requests, pages of a request]", 3)
-    _matrix(block_table, "block_table", B, block_table.shape[1], (torch.int32,))
-    _vector(lengths, "lengths", B, torch.int32)
-    if out is not None:
-        _matrix(out, "out", B, q.shape[1], (q.dtype,))
+    if dt not in _16:
+        _bad(f"q has type {dt}, expected float16 or bfloat16", 2)
+    B, n = q.shape
+    heads = n // cache.dim
+    ldq, ldt = _lead(q, "q", B, n, dt, dev), _table(block_table, B, dev)
+    width, at_lengths = block_table.shape[1], _vec(lengths, "lengths", B, torch.int32, dev)
+    ldo = n if out is None else _lead(out, "out", B, n, dt, dev)
     if lse is not None:
-        _matrix(lse, "lse", B, heads, (torch.float32,))
+        _lead(lse, "lse", B, heads, torch.float32, dev)
         if not lse.is_contiguous():
             _bad("lse must be contiguous", 3)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _bad(f"workspace must be contiguous, on GPU {dev}", 3)
+    ks, vs = cache.k_scale, cache.v_scale
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = q.new_empty((B, n))
         if workspace is None:
-            nbytes = _c.hts_paged_attn_workspace(B, heads, cache.desc, block_table.shape[1], window)
+            nbytes = cache.workspace_bytes(B, heads, width, window)
             if nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        elif not workspace.is_contiguous():
-            _bad("workspace must be contiguous", 3)
-        if B <= 1 and block_table.stride(0) < block_table.shape[1]:
-            block_table = block_table.as_strided(block_table.shape, (block_table.shape[1], 1))
-        _c.hts_paged_attn(heads, cache.desc, _rows(q), cache.k, cache.v, block_table, lengths,
-                          cache.dim ** -0.5 if scale is None else scale, _rows(out), cache.k_scale, cache.v_scale,
-                          window, lse, workspace)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        _c._check(_c.lib().hts_paged_attn(
+            _c._DT[dt], B, heads, cache._desc, q.data_ptr(), ldq, cache.k.data_ptr(), cache.v.data_ptr(),
+            None if ks is None else ks.data_ptr(), None if vs is None else vs.data_ptr(), block_table.data_ptr(), ldt,
+            width, at_lengths, cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo,
+            None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.nbytes, _c._current_stream(dev)))
     return out
 
 
@@ -332,6 +380,7 @@ class Norm:
 
 
 _NO_NORM = Norm("none")
+_norm_descs = {}
 
 
 def residual_norm(block: Optional[torch.Tensor], residual: Optional[torch.Tensor], post: Optional[Norm] = None,
@@ -347,39 +396,54 @@ def residual_norm(block: Optional[torch.Tensor], residual: Optional[torch.Tensor
     ref = block if block is not None else residual
     if ref is None or ref.dim() != 2:
         _bad("block or residual must be a [rows, width] matrix", 3)
-    (M, N), dev = ref.shape, ref.device
+    (M, N), dev = ref.shape, _gpu(ref, "block" if ref is block else "residual")
     post, pre = post or _NO_NORM, pre or _NO_NORM
-    kinds = _choice(_NORMS, post.kind, "norm"), _choice(_NORMS, pre.kind, "norm")
-    act = _choice(_GATES, gate_act, "gate")
-    _here(dev, block=block, residual=residual, gate=gate, residual_out=residual_out, out=out, post_weight=post.weight,
-          post_bias=post.bias, pre_weight=pre.weight, pre_bias=pre.bias)
     dt = block.dtype if block is not None else out.dtype if out is not None else out_dtype or residual.dtype
     if dt not in _16:
         _bad(f"block and out of type {dt}: float16 or bfloat16 are taken", 2)
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
+    if rdt is not dt and rdt is not torch.float32:
+        _bad(f"the residual has type {rdt}, expected {dt} or float32", 2)
+    key = (dt, rdt, post.kind, pre.kind, post.eps, pre.eps, scale, gate_act)
+    desc = _norm_descs.get(key)
+    if desc is None:
+        if len(_norm_descs) > 1000:
+            _norm_descs.clear()
+        desc = _norm_descs[key] = ctypes.byref(_c.hts_norm_desc(
+            _c._dt(dt), _c._dt(rdt), _choice(_NORMS, post.kind, "norm"), _choice(_NORMS, pre.kind, "norm"), post.eps,
+            pre.eps, scale, _choice(_GATES, gate_act, "gate")))
+    at_block = at_gate = at_r = None
+    ldb = ldg = ldr = 0
     if block is not None:
-        _matrix(block, "block", M, N, (dt,))
-    if residual is not None:
-        _matrix(residual, "residual", M, N, (dt, torch.float32))
-    if residual_out is not None:
-        _matrix(residual_out, "residual_out", M, N, (rdt,))
-    if out is not None:
-        _matrix(out, "out", M, N, (dt,))
+        at_block, ldb = block.data_ptr(), _lead(block, "block", M, N, dt, dev)
     if gate is not None:
+        at_gate = gate.data_ptr()
         if gate.dim() == 1:
-            _vector(gate, "gate", N, dt)
+            _vec(gate, "gate", N, dt, dev)
         else:
-            _matrix(gate, "gate", M, N, (dt,))
-    for n, name in ((post, "post"), (pre, "pre")):
-        for t, what in ((n.weight, "weight"), (n.bias, "bias")):
-            if t is not None:
-                _vector(t, f"{name}_{what}", N, dt)
-    desc = _c.hts_norm_desc(_c._dt(dt), _c._dt(rdt), kinds[0], kinds[1], post.eps, pre.eps, scale, act)
+            ldg = _lead(gate, "gate", M, N, dt, dev)
+    if residual is not None:
+        at_r, ldr = residual.data_ptr(), _lead(residual, "residual", M, N, rdt, dev)
+    w = [None if t is None else _vec(t, name, N, dt, dev)
+         for t, name in ((post.weight, "post weight"), (post.bias, "post bias"), (pre.weight, "pre weight"),
+                         (pre.bias, "pre bias"))]
     with _scope(dev, stream):
-        if residual_out is None and keep_residual:
-            residual_out = torch.empty((M, N), dtype=rdt, device=dev)
-        if out is None and kinds[1]:
-            out = torch.empty((M, N), dtype=dt, device=dev)
-        r = [None if t is None else _rows(t) for t in (block, gate, residual, residual_out, out)]
-        _c.hts_residual_norm(desc, M, N, r[0], post.weight, post.bias, r[1], r[2], pre.weight, pre.bias, r[3], r[4])
+        at_ro = at_y = None
+        ldro = ldy = N
+        if residual_out is not None:
+            ldro = _lead(residual_out, "residual_out", M, N, rdt, dev)
+        elif keep_residual:
+            residual_out = torch.empty_like(ref) if ref.dtype is rdt and ref.is_contiguous() \
+                else torch.empty((M, N), dtype=rdt, device=ref.device)
+        if out is not None:
+            ldy = _lead(out, "out", M, N, dt, dev)
+        elif pre.kind != "none":
+            out = torch.empty_like(ref) if ref.dtype is dt and ref.is_contiguous() \
+                else torch.empty((M, N), dtype=dt, device=ref.device)
+        if residual_out is not None:
+            at_ro = residual_out.data_ptr()
+        if out is not None:
+            at_y = out.data_ptr()
+        _c._check(_c.lib().hts_residual_norm(desc, M, N, at_block, ldb, w[0], w[1], at_gate, ldg, at_r, ldr, w[2], w[3],
+                                             at_ro, ldro, at_y, ldy, _c._current_stream(dev)))
     return residual_out, out
