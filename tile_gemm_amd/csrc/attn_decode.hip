@@ -20,10 +20,14 @@
 // with V rounds them no further than 2^-16: the matrix cores are idle most of the time.
 // K's registers are reloaded for the next step as soon as the scores are out, V's as soon as O is.
 //
-// Few requests with long contexts would leave the chip idle, so the tokens of a request are split
-// over workgroups: every workgroup reads the lengths, derives the same chunk size (total / target)
-// and finds its request and chunk by a scan; chunks of split requests leave (O, m, l) in the
-// workspace, and a second kernel joins them in order.
+// The work is divided evenly: per cache head, the steps of all requests in a row are cut into as
+// many equal runs as there are workgroups for that head on the chip at once.  Every workgroup reads
+// the lengths, finds its run by a scan over them and goes through the requests in it; a request that
+// lies whole in one run is written at once, the parts of one that is cut leave (O, m, l) in the
+// workspace, and a second kernel joins them in order.  All workgroups then end together, whatever the
+// mix of lengths (one request and chunk to a workgroup left a tail: 64 requests of 128 .. 8191 tokens).
+#include <type_traits>
+
 #include "serve_device.h"
 #include "serve_internal.h"
 
@@ -34,6 +38,14 @@ constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Read of an index that is the same in all lanes, by way of the scalar cache: a vector load would
+// have to wait for every load of K and V before it (they return in order).  Nothing writes these
+// arrays while the kernel runs.
+typedef const __attribute__((address_space(4))) int32_t* ScalarPtr;
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p, int64_t i) {
+    return reinterpret_cast<ScalarPtr>(reinterpret_cast<uintptr_t>(p))[i];
+}
 
 // Two E4M3 bytes (the low or high half of w) to two 16-bit values, exactly.
 template <typename T, bool HI> __device__ __forceinline__ uint32_t pair_e4m3(uint32_t w);
@@ -50,21 +62,23 @@ template <> __device__ __forceinline__ uint32_t pair_e4m3<F16T, true>(uint32_t w
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
 }
 
+constexpr uint32_t kBufferEnd = 0xFFFFF000u;   // past every offset in a half step (15 token strides and a head)
+
 // N 16-bit values (N/2 words) as stored: 16-bit values, or E4M3 bytes until they are used.
 template <bool C8, int N> struct Raw {
     static constexpr int words = C8 ? N / 4 : N / 2;
     uint32_t w[words];
-    __device__ __forceinline__ void load(const char* p) {
-        if (words == 4) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t from, uint32_t lane_off, uint32_t off) {
+        if constexpr (words == 4) {
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, lane_off, off, 0));
 #pragma unroll
             for (int i = 0; i < words; ++i) w[i] = v[i];
-        } else if (words == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
+        } else if constexpr (words == 2) {
+            const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(from, lane_off, off, 0));
             w[0] = v.x;
-            w[words - 1] = v.y;
+            w[1] = v.y;
         } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(from, lane_off, off, 0);
         }
     }
     __device__ __forceinline__ void clear() {
@@ -77,74 +91,58 @@ template <bool C8, int N> struct Raw {
     }
 };
 
-// Tokens of request b: [start, len), counted from begin = start rounded down to a step.
+// Tokens of request b: [start, len), counted from begin = start rounded down to a step of 32.
 struct Span {
     uint32_t start, begin, len;
-    __device__ __forceinline__ uint32_t size() const { return len - begin; }
+    __device__ __forceinline__ uint32_t steps() const { return max(1u, (len - begin + 31) / 32); }
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int32_t length) {
     Span s;
-    s.len = min((uint32_t)max(a.lengths[b], 0), a.cap);
+    s.len = min((uint32_t)max(length, 0), a.cap);
     s.start = a.window && s.len > a.window ? s.len - a.window : 0;
     s.begin = s.start & ~31u;
     return s;
 }
 
-struct Place {
-    int b;                       // request, -1: this workgroup has no work
-    uint32_t split, count, slot, chunk;
-};
+__device__ __forceinline__ uint64_t uniform64(uint64_t x) {
+    return ((uint64_t)uniform((uint32_t)(x >> 32)) << 32) | uniform((uint32_t)x);
+}
 
-// The x-th workgroup's request and chunk.  Every wave of every workgroup finds the same division.
-__device__ __forceinline__ Place find_place(const AttnArgs& a, uint32_t x, int lane) {
-    const int per = (a.B + 63) / 64, b0 = lane * per;
-    uint64_t total = 0;
-    for (int i = 0; i < per; ++i)
-        if (b0 + i < a.B) total += span_of(a, b0 + i).size();
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-    total = ((uint64_t)uniform((uint32_t)(total >> 32)) << 32) | uniform((uint32_t)total);
-    const uint64_t want = (total / (uint32_t)a.target + 32) & ~uint64_t(31);
-    // (lengths are below 2^31: a chunk of that size splits nothing)
-    const uint32_t chunk = (uint32_t)min(max(want, (uint64_t)a.min_chunk), uint64_t(1) << 31);
-    uint32_t n = 0, ns = 0;
-    for (int i = 0; i < per; ++i)
-        if (b0 + i < a.B) {
-            const uint32_t k = max(1u, (span_of(a, b0 + i).size() + chunk - 1) / chunk);
-            n += k;
-            ns += k > 1 ? k : 0;
-        }
-    uint32_t in = n, ins = ns;
+// A workgroup's run of steps: from step `off` of request b on, `left` steps in all; per: a full run.
+struct Run {
+    int b;
+    uint32_t off;
+    uint64_t left, per;
+};
+__device__ __forceinline__ Run find_run(const AttnArgs& a, uint32_t x, int lane) {
+    const int each = (a.B + 63) / 64, b0 = lane * each;
+    uint64_t mine = 0;
+    for (int i = 0; i < each; ++i)
+        if (b0 + i < a.B) mine += span_of(a, a.lengths[b0 + i]).steps();
+    uint64_t in = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = __shfl_up(in, o), us = __shfl_up(ins, o);
-        if (lane >= o) {
-            in += u;
-            ins += us;
-        }
+        const uint64_t u = __shfl_up(in, o);
+        if (lane >= o) in += u;
     }
-    Place p;
-    p.chunk = chunk;
-    p.b = -1;
-    const uint64_t past = __ballot(in > x);
-    if (!past) return p;
-    const int owner = __builtin_ctzll(past);
-    uint32_t base = __builtin_amdgcn_readlane(in - n, owner), slot = __builtin_amdgcn_readlane(ins - ns, owner);
-    for (int i = 0; i < per; ++i) {
-        const int b = owner * per + i;
-        if (b >= a.B) break;
-        const uint32_t k = max(1u, (span_of(a, b).size() + chunk - 1) / chunk);
-        if (x < base + k) {
-            p.b = b;
-            p.split = x - base;
-            p.count = k;
-            p.slot = slot;
-            break;
-        }
-        base += k;
-        slot += k > 1 ? k : 0;
+    const uint64_t total = uniform64(__shfl(in, 63));
+    const uint64_t runs = min((uint64_t)gridDim.x, (total + a.min_steps - 1) / a.min_steps);
+    Run r;
+    r.per = (total + runs - 1) / runs;
+    const uint64_t pos = x * r.per;
+    r.left = pos < total ? min(r.per, total - pos) : 0;
+    if (!r.left) return r;
+    const int owner = __builtin_ctzll(__ballot(in > pos));
+    uint64_t at = uniform64(__shfl(in - mine, owner));
+    r.b = owner * each;
+    for (;;) {                                      // ends: the owner's requests hold step pos
+        const uint32_t n = span_of(a, scalar_load(a.lengths, r.b)).steps();
+        if (pos < at + n) break;
+        at += n;
+        ++r.b;
     }
-    return p;
+    r.off = (uint32_t)(pos - at);
+    return r;
 }
 
 // DP: the head size rounded up to 64, 128 or 256; FULL: it is the head size.
@@ -164,19 +162,38 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     const int group = a.q_heads / a.k_heads;
     const int heads = min(16, group - ht * 16), head0 = hk * group + ht * 16;
 
-    Place p{(int)blockIdx.x, 0, 1, 0, 0};
+    Run run{(int)blockIdx.x, 0, ~uint64_t(0), ~uint64_t(0)};
+    if (a.part_o) run = find_run(a, blockIdx.x, lane);
+    const char* kbase = (const char*)a.kc + (int64_t)hk * a.head_stride * ES;
+    const char* vbase = (const char*)a.vc + (int64_t)hk * a.head_stride * ES;
+    // A half step is read through a buffer resource at its first token: a scalar base, one 32-bit offset per lane.
+    // Entries past the head's end get an offset past the buffer's: they read as zero, and nothing is fetched.
+    const uint32_t k_lane = ((uint32_t)c * (uint32_t)a.token_stride + 8 * g) * ES;
+    const uint32_t v_lane = ((uint32_t)(4 * g) * (uint32_t)a.token_stride + VEC * c) * ES;
+    const uint32_t v_step = (uint32_t)a.token_stride * ES, page_mask = (1u << a.page_shift) - 1;
+    const float s_scale = a.scale * kLog2e * (C8 && a.k_scale ? a.k_scale[hk] : 1.0f);
+    const float v_scale = C8 && a.v_scale ? a.v_scale[hk] : 1.0f;
+
+    for (uint32_t slot = 2 * blockIdx.x; run.left; slot |= 1) {   // one request, or the part of it in this run
+    const int b = run.b;
+    const Span sp = span_of(a, scalar_load(a.lengths, b));
+    const uint32_t steps = sp.steps(), n_steps = (uint32_t)min((uint64_t)(steps - run.off), run.left);
+    const bool whole_request = n_steps == steps;
+    const uint32_t first = sp.begin + 32 * run.off;
+    const uint32_t last = min(sp.len, first + 32 * n_steps);
     if (a.part_o) {
-        p = find_place(a, blockIdx.x, lane);
-        if (p.b < 0) return;
+        if (run.off == 0 && y == 0 && tid == 0)
+            a.plan[b] = uint2{slot, 1 + (uint32_t)((steps - n_steps + run.per - 1) / run.per)};
+        run.left -= n_steps;
+        run.off = 0;
+        ++run.b;
+    } else {
+        run.left = 0;
     }
-    const Span sp = span_of(a, p.b);
-    const uint32_t first = sp.begin + p.split * p.chunk;
-    const uint32_t last = p.count > 1 && p.split + 1 < p.count ? first + p.chunk : sp.len;
-    if (a.part_o && y == 0 && p.split == 0 && tid == 0) a.plan[p.b] = uint2{p.slot, p.count};
 
     u32x4 q[NK];
     {
-        const uint16_t* row = a.Q + p.b * a.ldq + (int64_t)(head0 + c) * a.dim;
+        const uint16_t* row = a.Q + b * a.ldq + (int64_t)(head0 + c) * a.dim;
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             q[k] = u32x4{0, 0, 0, 0};
@@ -184,48 +201,48 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             if (c < heads && (FULL || d < a.dim)) q[k] = ld16(row + d);
         }
     }
+    const int32_t* table = a.table + b * a.ldt;
 
-    const int32_t* table = a.table + p.b * a.ldt;
-    const char* kbase = (const char*)a.kc + (int64_t)hk * a.head_stride * ES;
-    const char* vbase = (const char*)a.vc + (int64_t)hk * a.head_stride * ES;
-    const uint32_t k_lane = ((uint32_t)c * (uint32_t)a.token_stride + 8 * g) * ES;
-    const uint32_t v_lane = ((uint32_t)(4 * g) * (uint32_t)a.token_stride + VEC * c) * ES;
-    const uint32_t v_step = (uint32_t)a.token_stride * ES, page_mask = (1u << a.page_shift) - 1;
-    const float s_scale = a.scale * kLog2e * (C8 && a.k_scale ? a.k_scale[hk] : 1.0f);
-
-    // the two 16-token halves of the step at t: byte offset of the first token, and whether a page holds it
+    // the two 16-token halves of the step at t: the page's id (requested a step ahead), then the byte offset of
+    // the half's first token and whether a page holds it
     struct Half {
         int64_t off;
         bool ok;
     };
-    const auto half = [&](uint32_t t) {
+    const uint32_t last_page = (a.cap - 1) >> a.page_shift;   // ids past it are asked for, but never used
+    const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
+    const auto half = [&](uint32_t t, int32_t id) {
         Half h;
-        const uint32_t j = t >> a.page_shift;
-        const int64_t id = t < a.cap ? table[j] : -1;
         h.ok = id >= 0 && id < a.pages;
         h.off = ((h.ok ? id : 0) * a.page_stride + (int64_t)(t & page_mask) * a.token_stride) * ES;
         return h;
     };
     Raw<C8, 8> kr[2][NK];
     Raw<C8, VEC> vr[NH][8];
+    const auto resource = [&](const char* base, int64_t off) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base) + off, (short)0, (int)kBufferEnd,
+                                                 0x00020000);
+    };
     const auto load_k = [&](const Half* h) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
+            const auto from = resource(kbase, h[j].off);
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                if (FULL || 32 * k + 8 * g < a.dim) kr[j][k].load(kbase + h[j].off + (k_lane + 32 * k * ES));
-                else kr[j][k].clear();
-            }
+            for (int k = 0; k < NK; ++k)
+                kr[j][k].load(from, FULL || 32 * k + 8 * g < a.dim ? k_lane + 32 * k * ES : kBufferEnd, 0);
+        }
     };
     const auto load_v = [&](const Half* h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const auto from = resource(vbase, h[j].off);
 #pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                if (FULL || 128 * n + VEC * c < a.dim)
-                    vr[n][i].load(vbase + h[i >> 2].off + (v_lane + (i & 3) * v_step + 128 * n * ES));
-                else vr[n][i].clear();
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+                    vr[n][4 * j + i].load(from, FULL || 128 * n + VEC * c < a.dim ? v_lane + 128 * n * ES : kBufferEnd,
+                                          i * v_step);
+        }
     };
 
     f32x4 o[NH][VEC];
@@ -236,19 +253,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     float m = -INFINITY, ref = 0.0f, l = 0.0f;   // of head c; l: this lane's tokens only
 
     uint32_t t = first + 32 * wave;
-    Half now[2], next[2];
-    if (t < last) {
-        now[0] = half(t);
-        now[1] = half(t + 16);
-        load_k(now);
-        load_v(now);
-    }
-    for (; t < last; t += 32 * kWaves) {
+    Half now[2];
+    int32_t ahead[2];
+    // one step of 32 tokens; MORE: the wave has another step, whose loads are issued on the way.  (The last step is
+    // a copy of its own: behind a branch around the loads the compiler would wait for V where K is used.)
+    const auto step = [&](auto more) {
+        constexpr bool MORE = decltype(more)::value;
+        Half next[2];
         const uint32_t tn = t + 32 * kWaves;
-        const bool more = tn < last && tn > t;
-        if (more) {
-            next[0] = half(tn);
-            next[1] = half(tn + 16);
+        if (MORE) {
+            next[0] = half(tn, ahead[0]);
+            next[1] = half(tn + 16, ahead[1]);
         }
         f32x4 s[2];
 #pragma unroll
@@ -261,7 +276,11 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
                 s[j] = mfma_dense<T>(x, q[k], s[j]);
             }
         }
-        if (more) load_k(next);
+        if (MORE) {
+            load_k(next);
+            ahead[0] = page_id(tn + 32 * kWaves);
+            ahead[1] = page_id(tn + 32 * kWaves + 16);
+        }
         // outside the span, or in no page: no weight (and no value: 0 * NaN is NaN)
         const bool whole = t >= sp.start && t + 32 <= last && t + 32 > t && now[0].ok && now[1].ok;
 #pragma unroll
@@ -326,9 +345,22 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
                 o[n][2 * w] = mfma_dense<T>(even, lo, o[n][2 * w]);
                 o[n][2 * w + 1] = mfma_dense<T>(odd, lo, o[n][2 * w + 1]);
             }
-        if (more) load_v(next);
-        now[0] = next[0];
-        now[1] = next[1];
+        if (MORE) {
+            load_v(next);
+            now[0] = next[0];
+            now[1] = next[1];
+            t = tn;
+        }
+    };
+    if (t < last) {
+        now[0] = half(t, page_id(t));
+        now[1] = half(t + 16, page_id(t + 16));
+        ahead[0] = page_id(t + 32 * kWaves);
+        ahead[1] = page_id(t + 32 * kWaves + 16);
+        load_k(now);
+        load_v(now);
+        while (last - t > 32 * kWaves) step(std::true_type());
+        step(std::false_type());
     }
 
     // the four waves' parts of each head, in order
@@ -343,9 +375,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) all = fmaxf(all, lds_m[w][c]);
     const float f = m == -INFINITY ? 0.0f : exp2f(m - all);
-    const bool split = p.count > 1;
-    const int64_t part = ((int64_t)(p.slot + p.split) * gridDim.y + y) * a.tile_heads;
-    const float v_scale = C8 && a.v_scale ? a.v_scale[hk] : 1.0f;
+    const int64_t part = ((int64_t)slot * gridDim.y + y) * a.tile_heads;
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
         if (n) __syncthreads();
@@ -370,18 +400,20 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
                 den += lds_m[w][h] == -INFINITY ? 0.0f : lds_l[w][h] * exp2f(lds_m[w][h] - top);
-            if (split) {
+            if (!whole_request) {
                 *reinterpret_cast<f32x4*>(a.part_o + (part + h) * a.dim + at) = sum;
                 if (at == 0) a.part_ml[part + h] = float2{top, den};
             } else {
                 const float inv = den == 0.0f ? 0.0f : v_scale / den;
-                uint16_t* out = a.O + p.b * a.ldo + (int64_t)(head0 + h) * a.dim + at;
+                uint16_t* out = a.O + b * a.ldo + (int64_t)(head0 + h) * a.dim + at;
                 *reinterpret_cast<uint2*>(out) = uint2{narrow<T>(sum[0] * inv) | (narrow<T>(sum[1] * inv) << 16),
                                                        narrow<T>(sum[2] * inv) | (narrow<T>(sum[3] * inv) << 16)};
                 if (at == 0 && a.lse)
-                    a.lse[(int64_t)p.b * a.q_heads + head0 + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
+                    a.lse[(int64_t)b * a.q_heads + head0 + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
             }
         }
+    }
+    if (run.left) __syncthreads();       // the next request's parts go to the same LDS
     }
 }
 
@@ -397,7 +429,10 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a) {
     const int group = a.q_heads / a.k_heads, hk = h / group, gh = h - hk * group;
     const int y = hk * a.head_tiles + gh / 16, rows = a.k_heads * a.head_tiles;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const auto part = [&](uint32_t i) { return ((int64_t)(plan.x + i) * rows + y) * a.tile_heads + (gh & 15); };
+    // the first part's slot, then the first slot of each run after it
+    const auto part = [&](uint32_t i) {
+        return ((int64_t)(i ? 2 * (plan.x / 2 + i) : plan.x) * rows + y) * a.tile_heads + (gh & 15);
+    };
     float top = -INFINITY;
     for (uint32_t i = lane; i < plan.y; i += 64) top = fmaxf(top, a.part_ml[part(i)].x);
 #pragma unroll
@@ -433,7 +468,7 @@ __global__ __launch_bounds__(64 * kWaves) void join_kernel(AttnArgs a) {
 
 template <typename T, bool C8>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.part_o ? a.B + a.target : a.B), (unsigned)(a.k_heads * a.head_tiles)), block(64 * kWaves);
+    const dim3 grid((unsigned)(a.part_o ? a.runs : a.B), (unsigned)(a.k_heads * a.head_tiles)), block(64 * kWaves);
     if (a.dim == 64) attn_kernel<T, C8, 64, true><<<grid, block, 0, s>>>(a);
     else if (a.dim < 64) attn_kernel<T, C8, 64, false><<<grid, block, 0, s>>>(a);
     else if (a.dim == 128) attn_kernel<T, C8, 128, true><<<grid, block, 0, s>>>(a);

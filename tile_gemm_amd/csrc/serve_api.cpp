@@ -94,11 +94,11 @@ hts_status check_table(const int32_t* table, int64_t B, int64_t ldt, int64_t wid
     return B ? check_aligned(table, 4, "block_table") : HTS_OK;
 }
 
-// How hts_paged_attn divides its work.  Workgroups in all: 4 to a CU (they hold 3 or 4 there), divided by the
-// cache heads and head tiles, each of which takes all requests.
+// How hts_paged_attn divides its work: runs per cache head and tile of 16 query heads, as many as the chip
+// holds workgroups of them at once (each CU holds three).
 struct AttnPlan {
-    int32_t head_tiles, tile_heads, target;
-    uint32_t cap, window, min_chunk;
+    int32_t head_tiles, tile_heads, runs;
+    uint32_t cap, window, min_steps;
     bool split;
     uint64_t plan_bytes, ml_bytes, bytes;
 };
@@ -109,13 +109,14 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     p.tile_heads = std::min(group, 16);
     p.cap = (uint32_t)std::min<int64_t>(width * kv->page, kInt32 - 1);
     p.window = (uint32_t)std::min<int64_t>(window, kInt32 - 1);
-    p.min_chunk = 256;
+    p.min_steps = 8;
     const int64_t rows = (int64_t)kv->heads * p.head_tiles;
-    p.target = (int32_t)((1024 + rows - 1) / rows);
     const uint64_t most = window ? std::min<uint64_t>(p.cap, (uint64_t)p.window + 31) : p.cap;
-    p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > p.min_chunk;
+    const uint64_t steps = (uint64_t)B * ((most + 31) / 32);
+    p.runs = (int32_t)std::min<uint64_t>(std::max<int64_t>(1, 768 / rows), (steps + p.min_steps - 1) / p.min_steps);
+    p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > 256;
     if (p.split) {
-        const uint64_t parts = 2 * (uint64_t)p.target * rows * p.tile_heads;
+        const uint64_t parts = 2 * (uint64_t)p.runs * rows * p.tile_heads;
         p.plan_bytes = (8 * (uint64_t)B + 255) & ~uint64_t(255);
         p.ml_bytes = (8 * parts + 255) & ~uint64_t(255);
         p.bytes = p.plan_bytes + p.ml_bytes + 4 * parts * kv->dim;
@@ -437,8 +438,8 @@ hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_k
     a.cap = p.cap;
     a.head_tiles = p.head_tiles;
     a.tile_heads = p.tile_heads;
-    a.target = p.target;
-    a.min_chunk = p.min_chunk;
+    a.runs = p.runs;
+    a.min_steps = p.min_steps;
     if (p.split && workspace && workspace_bytes >= p.bytes) {
         char* ws = static_cast<char*>(workspace);
         a.plan = reinterpret_cast<uint2*>(ws);

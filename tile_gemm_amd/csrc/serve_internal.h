@@ -61,16 +61,15 @@ struct AttnArgs {
     int64_t ldo;
     float* lse;
     int32_t head_tiles, tile_heads;   // tiles of 16 query heads to a cache head; heads of a tile (<= 16)
-    // Split over the length (part_o not NULL): chunks of total / target tokens, at least min_chunk, in at
-    // most 2 * target parts of split requests (a request of e tokens in chunks of c > total / target has
-    // ceil(e / c) <= 2 e / c of them, where it has more than one).
-    int32_t target;
-    uint32_t min_chunk;
-    uint2* plan;               // [B]: first part, number of chunks
-    float2* part_ml;           // [2 target][k_heads * head_tiles][tile_heads]
+    // Split over the length (part_o not NULL): the steps of 32 tokens of all requests, cut into `runs` equal
+    // runs of at least min_steps; a run leaves at most two parts (of its first and its last request).
+    int32_t runs;
+    uint32_t min_steps;
+    uint2* plan;               // [B]: first part's slot, number of parts
+    float2* part_ml;           // [2 runs][k_heads * head_tiles][tile_heads]
     float* part_o;             // the same, [dim]
 };
-// Requests whose division every wave can find in one pass; more run unsplit.
+// Requests whose runs every wave finds by one scan; more run unsplit.
 constexpr int64_t kMaxSplitRequests = 4096;
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
