@@ -95,10 +95,10 @@ hts_status check_table(const int32_t* table, int64_t B, int64_t ldt, int64_t wid
 }
 
 // How hts_paged_attn divides its work: runs per cache head and tile of 16 query heads, as many as the chip
-// holds workgroups of them at once (each CU holds three).
+// holds workgroups of them at once.
 struct AttnPlan {
-    int32_t head_tiles, tile_heads, runs;
-    uint32_t cap, window, min_steps;
+    int32_t head_tiles, tile_heads, runs, target;
+    uint32_t cap, window;
     bool split;
     uint64_t plan_bytes, ml_bytes, bytes;
 };
@@ -109,12 +109,15 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     p.tile_heads = std::min(group, 16);
     p.cap = (uint32_t)std::min<int64_t>(width * kv->page, kInt32 - 1);
     p.window = (uint32_t)std::min<int64_t>(window, kInt32 - 1);
-    p.min_steps = 8;
     const int64_t rows = (int64_t)kv->heads * p.head_tiles;
     const uint64_t most = window ? std::min<uint64_t>(p.cap, (uint64_t)p.window + 31) : p.cap;
     const uint64_t steps = (uint64_t)B * ((most + 31) / 32);
-    p.runs = (int32_t)std::min<uint64_t>(std::max<int64_t>(1, 768 / rows), (steps + p.min_steps - 1) / p.min_steps);
-    p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > 256;
+    // 256 CUs hold three workgroups each; of those for heads above 128 entries two, but one streams as fast and
+    // leaves fewer parts (16 requests up to 8192, 16/4 heads of 256: 75 us with 256 runs, 88 with 768)
+    p.target = (int32_t)std::max<int64_t>(1, (kv->dim > 128 ? 256 : 768) / rows);
+    const uint64_t least = std::min<uint64_t>(std::max<uint64_t>(3 * steps / p.target, 8), 16);   // as in the kernel
+    p.runs = (int32_t)std::min<uint64_t>(p.target, (steps + least - 1) / least);
+    p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > 256 && steps < (uint64_t)kInt32;
     if (p.split) {
         const uint64_t parts = 2 * (uint64_t)p.runs * rows * p.tile_heads;
         p.plan_bytes = (8 * (uint64_t)B + 255) & ~uint64_t(255);
@@ -439,7 +442,7 @@ hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_k
     a.head_tiles = p.head_tiles;
     a.tile_heads = p.tile_heads;
     a.runs = p.runs;
-    a.min_steps = p.min_steps;
+    a.target = p.target;
     if (p.split && workspace && workspace_bytes >= p.bytes) {
         char* ws = static_cast<char*>(workspace);
         a.plan = reinterpret_cast<uint2*>(ws);

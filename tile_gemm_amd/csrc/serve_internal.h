@@ -61,10 +61,10 @@ struct AttnArgs {
     int64_t ldo;
     float* lse;
     int32_t head_tiles, tile_heads;   // tiles of 16 query heads to a cache head; heads of a tile (<= 16)
-    // Split over the length (part_o not NULL): the steps of 32 tokens of all requests, cut into `runs` equal
-    // runs of at least min_steps; a run leaves at most two parts (of its first and its last request).
-    int32_t runs;
-    uint32_t min_steps;
+    // Split over the length (part_o not NULL): the steps of 32 tokens of all requests, cut into at most
+    // `runs` equal runs; a run leaves at most two parts (of its first and its last request).
+    uint32_t target;           // runs of a cache head that the chip holds at once
+    int32_t runs;              // at most: fewer where the table's width bounds the steps
     uint2* plan;               // [B]: first part's slot, number of parts
     float2* part_ml;           // [2 runs][k_heads * head_tiles][tile_heads]
     float* part_o;             // the same, [dim]
