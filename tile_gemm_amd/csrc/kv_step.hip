@@ -17,19 +17,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
 
-struct Request {
-    int64_t c, a, have, fresh, len;
-};
-
-__device__ __forceinline__ Request request(const KvStepArgs& g, int b) {
-    Request r;
-    const int64_t cap = g.width << g.page_shift, up = (1 << g.page_shift) - 1;
-    r.c = max(g.cached[b], 0);
-    r.a = max(g.added[b], 0);
-    r.len = min(r.c + r.a, cap);
-    r.have = (min(r.c, cap) + up) >> g.page_shift;
-    r.fresh = ((r.len + up) >> g.page_shift) - r.have;
-    return r;
+// pages that hold n tokens (n cut to the table's width)
+__device__ __forceinline__ int64_t pages_of(const KvStepArgs& g, int64_t n) {
+    return (min(n, g.width << g.page_shift) + (1 << g.page_shift) - 1) >> g.page_shift;
 }
 
 // Last request b with first[b] <= x (first is non-decreasing, first[0] <= x).
@@ -42,20 +32,28 @@ __device__ __forceinline__ int find(const uint32_t* first, int n, uint32_t x) {
     return lo;
 }
 
+// EACH: requests of a thread
+template <int EACH>
 __global__ __launch_bounds__(kThreads) void kv_step_kernel(KvStepArgs g) {
     extern __shared__ uint32_t sums[];
     uint32_t* first = sums;              // first token of each request (saturated at 2^31 - 1)
     uint32_t* opened = sums + g.B;       // pages opened before each request (below 2^31)
+    uint32_t* held = sums + 2 * g.B;     // tokens in the cache
     __shared__ int64_t wave_a[kThreads / 64], wave_n[kThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per = (g.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, g.B), b1 = min(b0 + per, g.B);
-
+    const int64_t head = g.free_head ? max(g.free_head[0], 0) : 0;
+    int c[EACH], a[EACH];                // all loads go out before the first is used
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int b = tid * EACH + i;
+        c[i] = b < g.B ? max(g.cached[b], 0) : 0;
+        a[i] = b < g.B ? max(g.added[b], 0) : 0;
+    }
     int64_t sa = 0, sn = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request r = request(g, b);
-        sa += r.a;
-        sn += r.fresh;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        sa += a[i];
+        sn += pages_of(g, (int64_t)c[i] + a[i]) - pages_of(g, c[i]);
     }
     int64_t ia = sa, in = sn;            // inclusive sums over the wave
 #pragma unroll
@@ -81,17 +79,20 @@ __global__ __launch_bounds__(kThreads) void kv_step_kernel(KvStepArgs g) {
         all_a += wave_a[w];
         all_n += wave_n[w];
     }
-    const int64_t head = g.free_head ? max(g.free_head[0], 0) : 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request r = request(g, b);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int b = tid * EACH + i;
+        if (b >= g.B) break;
         first[b] = (uint32_t)min(ea, kMaxInt);
         opened[b] = (uint32_t)en;
+        held[b] = (uint32_t)c[i];
+        const int64_t len = (int64_t)c[i] + a[i];
         if (blockIdx.x == 0) {
-            g.lengths[b] = (int32_t)min(r.len, kMaxInt);
+            g.lengths[b] = (int32_t)min(min(len, g.width << g.page_shift), kMaxInt);
             g.starts[b] = (int32_t)min(ea, kMaxInt);
         }
-        ea += r.a;
-        en += r.fresh;
+        ea += a[i];
+        en += pages_of(g, len) - pages_of(g, c[i]);
     }
     if (blockIdx.x == 0 && tid == 0) {
         g.starts[g.B] = (int32_t)min(all_a, kMaxInt);
@@ -104,15 +105,14 @@ __global__ __launch_bounds__(kThreads) void kv_step_kernel(KvStepArgs g) {
         int64_t slot = -1, pos = -1;
         if (t < all_a) {
             const int b = find(first, g.B, (uint32_t)t);
-            const Request r = request(g, b);
-            pos = r.c + (t - first[b]);
-            const int64_t j = pos >> g.page_shift;
+            pos = (int64_t)held[b] + (t - first[b]);
+            const int64_t j = pos >> g.page_shift, have = pages_of(g, held[b]);
             if (j < g.width) {
                 int64_t id = -1;
-                if (j < r.have) {
+                if (j < have) {
                     id = g.table[b * g.ldt + j];
                 } else {
-                    const int64_t at = head + opened[b] + (j - r.have);
+                    const int64_t at = head + opened[b] + (j - have);
                     if (at < g.n_free) id = g.free_pages[at];
                 }
                 if (id >= 0) slot = (id << g.page_shift) + (pos & ((1 << g.page_shift) - 1));
@@ -124,9 +124,8 @@ __global__ __launch_bounds__(kThreads) void kv_step_kernel(KvStepArgs g) {
     }
     for (int64_t p = me; p < all_n; p += step) {
         const int b = find(opened, g.B, (uint32_t)p);
-        const Request r = request(g, b);
         const int64_t at = head + p;
-        g.table[b * g.ldt + r.have + (p - opened[b])] = at < g.n_free ? g.free_pages[at] : -1;
+        g.table[b * g.ldt + pages_of(g, held[b]) + (p - opened[b])] = at < g.n_free ? g.free_pages[at] : -1;
     }
 }
 
@@ -136,7 +135,10 @@ hipError_t launch_kv_step(const KvStepArgs& a, hipStream_t s) {
     const int64_t work = a.tokens > a.B ? a.tokens : a.B;
     const int64_t want = (work + 2 * kThreads - 1) / (2 * kThreads);
     const unsigned blocks = (unsigned)(want < 1 ? 1 : want > 512 ? 512 : want);
-    kv_step_kernel<<<dim3(blocks), dim3(kThreads), 2 * (size_t)a.B * sizeof(uint32_t), s>>>(a);
+    const size_t lds = 3 * (size_t)a.B * sizeof(uint32_t);
+    if (a.B <= kThreads) kv_step_kernel<1><<<dim3(blocks), dim3(kThreads), lds, s>>>(a);
+    else if (a.B <= 4 * kThreads) kv_step_kernel<4><<<dim3(blocks), dim3(kThreads), lds, s>>>(a);
+    else kv_step_kernel<kMaxStepRequests / kThreads><<<dim3(blocks), dim3(kThreads), lds, s>>>(a);
     return hipGetLastError();
 }
 

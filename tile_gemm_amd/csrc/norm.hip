@@ -1,145 +1,173 @@
 // The step between two blocks (hts_residual_norm): R' = R + scale * act(gate) * post(block),
 // Y = pre(R').
 //
-// One workgroup per row.  A thread keeps its entries of the row (8 per chunk) in registers as
-// floats, so the row is read once and every statistic -- the post norm's, then the pre norm's over
-// the sum -- is a reduction over registers; a layer norm's variance is summed around its mean.
-// Bound by HBM: block, R and a per-token gate in, R' and Y out, once each.
+// A row is held in registers as floats, 8 entries per chunk and thread, so it is read once and every
+// statistic -- the post norm's, then the pre norm's over the sum -- is a reduction over registers; a
+// layer norm's variance is summed around its mean.  Rows of up to 256 entries take 16 or 32 lanes of
+// a wave (no barrier, 16 or 8 rows per workgroup); longer ones a workgroup each.
+// Bound by HBM: block, R and a per-token gate in, R' and Y out, once each.  The outputs are written past the
+// caches' normal lines (non-temporal): another XCD will read them, and the inputs keep their place (1000 x
+// 16384: 24.4 us against 32 with ordinary stores).  16384 x 4096, layer norms on both sides and a sigmoid gate:
+// 138 us, 4.9 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.8 us.
 #include "serve_device.h"
 #include "serve_internal.h"
 
 namespace hts {
 namespace {
 
-// Sum over the NT threads of a row's workgroup.
-template <int NT> __device__ __forceinline__ float row_sum(float v, float* lds) {
-    v = wave_sum(v);
-    if (NT == 64) return v;
+// Sum over the threads of a row: LANES of a wave, or (LANES = 0) the whole workgroup.
+template <int LANES> __device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+    for (int o = (LANES ? LANES : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if (LANES) return v;
+    const int waves = blockDim.x >> 6;
+    if (waves == 1) return v;
     __syncthreads();                     // the last sum has been read by all
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) s += lds[w];
+    for (int w = 0; w < waves; ++w) s += lds[w];
     return s;
 }
 
-// x -> norm(x) * w + b over the row (columns past N hold 0 and stay 0 in the sums).
-template <typename T, int NT, int CH>
-__device__ __forceinline__ void norm_row(float (&x)[CH][8], int kind, float eps, const uint16_t* w, const uint16_t* b,
-                                         int N, float* lds) {
-    const float inv_n = 1.0f / (float)N;
-    if (kind == HTS_NORM_LAYER) {
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[c][e];
-        const float mean = row_sum<NT>(s, lds) * inv_n;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if ((c * NT + (int)threadIdx.x) * 8 < N)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[c][e] -= mean;
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(x[c][e], x[c][e], q);
-    const float r = 1.0f / sqrtf(row_sum<NT>(q, lds) * inv_n + eps);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int col = (c * NT + (int)threadIdx.x) * 8;
-        if (col < N) {
-            float wv[8], bv[8];
-            if (w) widen8<T>(ld16(w + col), wv);
-            if (b) widen8<T>(ld16(b + col), bv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float y = x[c][e] * r;
-                if (w) y *= wv[e];
-                if (b) y += bv[e];
-                x[c][e] = y;
-            }
-        }
-    }
-}
-
-template <typename T, bool R32, int NT, int CH>
-__global__ __launch_bounds__(NT) void residual_norm_kernel(NormArgs a) {
-    __shared__ float lds[NT / 64];
-    const int64_t m = blockIdx.x;
+template <typename T, bool R32, int LANES, int CH>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormArgs a) {
+    __shared__ float lds[16];
+    const int per_row = LANES ? LANES : blockDim.x, me = LANES ? threadIdx.x % LANES : threadIdx.x;
+    const int64_t m = LANES ? (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES : blockIdx.x;
+    if (LANES && m >= a.M) return;       // rows of one wave end apart: their shuffles stay within a row
     float x[CH][8];
+    // entry of chunk c; past the row's end a chunk holds zeros and stays out of the sums
+    const auto col = [&](int c) { return (c * per_row + me) * 8; };
+    const auto norm = [&](int kind, float eps, const uint16_t* w, const uint16_t* b) {
+        const float inv_n = 1.0f / (float)a.N;
+        // the weights' loads go out ahead of the sums
+        u32x4 wv[CH], bv[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (w && col(c) < a.N) wv[c] = ld16(w + col(c));
+            if (b && col(c) < a.N) bv[c] = ld16(b + col(c));
+        }
+        if (kind == HTS_NORM_LAYER) {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += x[c][e];
+            const float mean = row_sum<LANES>(s, lds) * inv_n;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (col(c) < a.N)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] -= mean;
+        }
+        float q = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(x[c][e], x[c][e], q);
+        const float r = 1.0f / sqrtf(row_sum<LANES>(q, lds) * inv_n + eps);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (col(c) < a.N) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[c][e] *= r;
+                if (w) {
+                    widen8<T>(wv[c], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] *= f[e];
+                }
+                if (b) {
+                    widen8<T>(bv[c], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] += f[e];
+                }
+            }
+    };
+
+    // everything the row needs is asked for at once
+    u32x4 rv[CH][R32 ? 2 : 1], gv[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int col = (c * NT + (int)threadIdx.x) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[c][e] = 0.0f;
-        if (a.block && col < a.N) widen8<T>(ld16(a.block + m * a.ldb + col), x[c]);
+        if (col(c) >= a.N) continue;
+        if (a.block) widen8<T>(ld16(a.block + m * a.ldb + col(c)), x[c]);
+        if (a.gate) gv[c] = ld16(a.gate + m * a.ldg + col(c));
+        if (a.R) {
+            const char* p = (const char*)a.R + (m * a.ldr + col(c)) * (R32 ? 4 : 2);
+            rv[c][0] = ld16(p);
+            if (R32) rv[c][R32 ? 1 : 0] = ld16(p + 16);
+        }
     }
-    if (a.post != HTS_NORM_NONE) norm_row<T, NT, CH>(x, a.post, a.post_eps, a.post_w, a.post_b, a.N, lds);
+    if (a.post != HTS_NORM_NONE) norm(a.post, a.post_eps, a.post_w, a.post_b);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int col = (c * NT + (int)threadIdx.x) * 8;
-        if (col < a.N) {
-            if (a.gate) {
-                float g[8];
-                widen8<T>(ld16(a.gate + m * a.ldg + col), g);
+        if (col(c) >= a.N) continue;
+        if (a.gate) {
+            float g[8];
+            widen8<T>(gv[c], g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float v = g[e];
-                    if (a.gate_act != HTS_GATE_PLAIN) {
-                        const float sg = 1.0f / (1.0f + expf(-v));
-                        v = a.gate_act == HTS_GATE_SIGMOID ? sg : v * sg;
-                    }
-                    x[c][e] *= v;
+            for (int e = 0; e < 8; ++e) {
+                float v = g[e];
+                if (a.gate_act != HTS_GATE_PLAIN) {
+                    const float sg = 1.0f / (1.0f + expf(-v));
+                    v = a.gate_act == HTS_GATE_SIGMOID ? sg : v * sg;
                 }
+                x[c][e] *= v;
             }
-            if (a.block)
+        }
+        if (a.block)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[c][e] *= a.scale;
-            if (a.R) {
-                float r[8];
-                if (R32) {
-                    const float* p = (const float*)a.R + m * a.ldr + col;
-                    *reinterpret_cast<f32x4*>(r) = *reinterpret_cast<const f32x4*>(p);
-                    *reinterpret_cast<f32x4*>(r + 4) = *reinterpret_cast<const f32x4*>(p + 4);
-                } else {
-                    widen8<T>(ld16((const uint16_t*)a.R + m * a.ldr + col), r);
-                }
+            for (int e = 0; e < 8; ++e) x[c][e] *= a.scale;
+        if (a.R) {
+            float r[8];
+            if (R32) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[c][e] += r[e];
+                for (int e = 0; e < 8; ++e) r[e] = __uint_as_float(rv[c][R32 ? e / 4 : 0][e & 3]);
+            } else {
+                widen8<T>(rv[c][0], r);
             }
-            if (a.R_out) {
-                if (R32) {
-                    float* p = (float*)a.R_out + m * a.ldro + col;
-                    *reinterpret_cast<f32x4*>(p) = f32x4{x[c][0], x[c][1], x[c][2], x[c][3]};
-                    *reinterpret_cast<f32x4*>(p + 4) = f32x4{x[c][4], x[c][5], x[c][6], x[c][7]};
-                } else {
-                    st16((uint16_t*)a.R_out + m * a.ldro + col, narrow8<T>(x[c]));
-                }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[c][e] += r[e];
+        }
+        if (a.R_out) {
+            char* p = (char*)a.R_out + (m * a.ldro + col(c)) * (R32 ? 4 : 2);
+            if (R32) {
+                stream16(p, u32x4{__float_as_uint(x[c][0]), __float_as_uint(x[c][1]), __float_as_uint(x[c][2]),
+                              __float_as_uint(x[c][3])});
+                stream16(p + 16, u32x4{__float_as_uint(x[c][4]), __float_as_uint(x[c][5]), __float_as_uint(x[c][6]),
+                                   __float_as_uint(x[c][7])});
+            } else {
+                stream16(p, narrow8<T>(x[c]));
             }
         }
     }
     if (!a.Y) return;
-    if (a.pre != HTS_NORM_NONE) norm_row<T, NT, CH>(x, a.pre, a.pre_eps, a.pre_w, a.pre_b, a.N, lds);
+    if (a.pre != HTS_NORM_NONE) norm(a.pre, a.pre_eps, a.pre_w, a.pre_b);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int col = (c * NT + (int)threadIdx.x) * 8;
-        if (col < a.N) st16(a.Y + m * a.ldy + col, narrow8<T>(x[c]));
-    }
+    for (int c = 0; c < CH; ++c)
+        if (col(c) < a.N) stream16(a.Y + m * a.ldy + col(c), narrow8<T>(x[c]));
 }
 
 template <typename T, bool R32>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.M);
     const int chunks = a.N / 8;
-    if (chunks <= 64) residual_norm_kernel<T, R32, 64, 1><<<grid, 64, 0, s>>>(a);
-    else if (chunks <= 256) residual_norm_kernel<T, R32, 256, 1><<<grid, 256, 0, s>>>(a);
-    else if (chunks <= 512) residual_norm_kernel<T, R32, 256, 2><<<grid, 256, 0, s>>>(a);
-    else if (chunks <= 1024) residual_norm_kernel<T, R32, 256, 4><<<grid, 256, 0, s>>>(a);
-    else residual_norm_kernel<T, R32, 1024, 4><<<grid, 1024, 0, s>>>(a);
+    const auto rows_of = [&](int per) { return dim3((unsigned)((a.M + per - 1) / per)); };
+    const auto threads = [&](int ch) { return dim3((unsigned)(((chunks + ch - 1) / ch + 63) / 64 * 64)); };
+    const dim3 grid((unsigned)a.M);
+    // Lanes of a wave for short rows (65536 x 128: 11.6 us against 22.1 with a workgroup of one wave each, 65536 x 256:
+    // 21.6 against 23.0).  Else one chunk per thread while the rows are few, for the shortest chain (1 x 4096:
+    // 2.8 us against 3.5 with two; 2048 x 4096: 12.1 against 12.6), two for many (16384 x 4096 with gate and layer
+    // norms: 138 against 152), four past 8192 entries (1000 x 16384: 21.3 against 24.4 with two).
+    const bool few = a.M <= 2048;
+    if (chunks <= 16) residual_norm_kernel<T, R32, 16, 1><<<rows_of(16), 256, 0, s>>>(a);
+    else if (chunks <= 32) residual_norm_kernel<T, R32, 32, 1><<<rows_of(8), 256, 0, s>>>(a);
+    else if (chunks <= 256 || (few && chunks <= 1024)) residual_norm_kernel<T, R32, 0, 1><<<grid, threads(1), 0, s>>>(a);
+    else if (chunks <= 1024 || (a.M <= 64 && chunks <= 2048))
+        residual_norm_kernel<T, R32, 0, 2><<<grid, threads(2), 0, s>>>(a);
+    else residual_norm_kernel<T, R32, 0, 4><<<grid, threads(4), 0, s>>>(a);
     return hipGetLastError();
 }
 

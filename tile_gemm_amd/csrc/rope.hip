@@ -29,7 +29,7 @@ template <typename T, int V> __device__ __forceinline__ void load_v(const uint16
 }
 template <typename T, int V> __device__ __forceinline__ void store_v(uint16_t* p, const float* f) {
     if (V == 8) {
-        st16(p, narrow8<T>(f));
+        stream16(p, narrow8<T>(f));
     } else {
         *reinterpret_cast<uint2*>(p) = uint2{narrow<T>(f[0]) | (narrow<T>(f[1]) << 16),
                                              narrow<T>(f[2]) | (narrow<T>(f[3]) << 16)};
@@ -43,8 +43,9 @@ template <int V> __device__ __forceinline__ void store_e4m3(uint8_t* p, const fl
     for (int i = 0; i < V; i += 4) *reinterpret_cast<uint32_t*>(p + i) = narrow4_e4m3(x + i);
 }
 
-// V pairs per item: entries [i, i+V) and [rot/2 + i, ...) (half) or [2i, 2i + 2V) (interleaved)
-template <typename T, int LAYOUT, int V, bool C8>
+// An item of a q or k head: P pairs, entries [i, i+P) and [rot/2 + i, ...) (half, P = 8 or 4) or the
+// 2P = 8 consecutive entries [2i, 2i + 8) (interleaved, P = 4); or 8 entries past the rotated part.
+template <typename T, int LAYOUT, int P, bool C8>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     __shared__ float cs[128], sn[128];
     const int64_t t = blockIdx.x;
@@ -59,48 +60,56 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
         cs[threadIdx.x] = c * a.magnitude;
         sn[threadIdx.x] = s * a.magnitude;
     }
-    __syncthreads();
-
-    const int turned = half / V, items = turned + (a.dim - a.rot) / 8;   // items of a q or k head
-    const int nq = a.q_heads * items, nk = a.k_heads * items;
     int64_t at = -1;                    // the token's place in the cache
     if (a.slots) {
         const int64_t slot = a.slots[t];
         if (slot >= 0 && slot < a.n_slots)
             at = (slot >> a.page_shift) * a.page_stride + (slot & ((1 << a.page_shift) - 1)) * a.token_stride;
     }
-    const bool write_k = a.Ko || at >= 0;
-    const int nv = at >= 0 ? a.k_heads * (a.dim / 8) : 0;
-    const int total = nq + (write_k ? nk : 0);
+    // items: all q heads, then all k heads, then v in chunks of 8
+    const int turned = half / P, items = turned + (a.dim - a.rot) / 8, per_v = a.dim / 8;
+    const int step = gridDim.y * kThreads, first = blockIdx.y * kThreads + threadIdx.x;
+    const int heads = a.q_heads + (a.Ko || at >= 0 ? a.k_heads : 0);
+    __syncthreads();
 
-    for (int it = threadIdx.x; it < total; it += kThreads) {
-        const bool is_q = it < nq;
-        const int x = is_q ? it : it - nq, h = x / items, w = x - h * items;
-        const uint16_t* src = (is_q ? a.Q + t * a.ldq : a.K + t * a.ldk) + h * a.dim;
-        const bool cached = !is_q && !a.Ko;
-        uint16_t* dst = is_q ? a.Qo + t * a.ldqo + h * a.dim
-                             : (cached ? (uint16_t*)a.kc + at + h * a.head_stride : a.Ko + t * a.ldko + h * a.dim);
-        uint8_t* dst8 = (uint8_t*)a.kc + at + h * a.head_stride;
-        const float scale = C8 && cached && a.k_scale ? a.k_scale[h] : 1.0f;
+    // (head, item) and its step, so that the loop has no division
+    int h = first / items, w = first - h * items;
+    const int dh = step / items, dw = step - dh * items;
+    for (; h < heads; h += dh) {
+        const bool is_q = h < a.q_heads, cached = !is_q && !a.Ko;
+        const int hh = is_q ? h : h - a.q_heads;
+        const uint16_t* src = (is_q ? a.Q + t * a.ldq : a.K + t * a.ldk) + hh * a.dim;
+        uint16_t* dst = is_q ? a.Qo + t * a.ldqo + hh * a.dim
+                             : (cached ? (uint16_t*)a.kc + at + hh * a.head_stride : a.Ko + t * a.ldko + hh * a.dim);
+        uint8_t* dst8 = (uint8_t*)a.kc + at + hh * a.head_stride;
+        const float scale = C8 && cached && a.k_scale ? a.k_scale[hh] : 1.0f;
         if (w < turned) {
-            const int i = w * V;
-            const int o0 = LAYOUT == HTS_ROPE_HALF ? i : 2 * i, o1 = LAYOUT == HTS_ROPE_HALF ? half + i : 2 * i + V;
-            float u[2 * V], r[2 * V];
-            load_v<T, V>(src + o0, u);
-            load_v<T, V>(src + o1, u + V);
+            const int i = w * P;
+            float u[2 * P], r[2 * P];
+            if constexpr (LAYOUT == HTS_ROPE_HALF) {
+                load_v<T, P>(src + i, u);
+                load_v<T, P>(src + half + i, u + P);
+            } else {
+                load_v<T, 8>(src + 2 * i, u);
+            }
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int ix = LAYOUT == HTS_ROPE_HALF ? e : 2 * e, iy = LAYOUT == HTS_ROPE_HALF ? V + e : 2 * e + 1;
+            for (int e = 0; e < P; ++e) {
+                const int ix = LAYOUT == HTS_ROPE_HALF ? e : 2 * e, iy = LAYOUT == HTS_ROPE_HALF ? P + e : 2 * e + 1;
                 const float c = cs[i + e], s = sn[i + e];
                 r[ix] = fmaf(u[ix], c, -(u[iy] * s));
                 r[iy] = fmaf(u[ix], s, u[iy] * c);
             }
-            if (C8 && cached) {
-                store_e4m3<V>(dst8 + o0, r, scale);
-                store_e4m3<V>(dst8 + o1, r + V, scale);
+            if constexpr (LAYOUT == HTS_ROPE_HALF) {
+                if (C8 && cached) {
+                    store_e4m3<P>(dst8 + i, r, scale);
+                    store_e4m3<P>(dst8 + half + i, r + P, scale);
+                } else {
+                    store_v<T, P>(dst + i, r);
+                    store_v<T, P>(dst + half + i, r + P);
+                }
             } else {
-                store_v<T, V>(dst + o0, r);
-                store_v<T, V>(dst + o1, r + V);
+                if (C8 && cached) store_e4m3<8>(dst8 + 2 * i, r, scale);
+                else store_v<T, 8>(dst + 2 * i, r);
             }
         } else {
             const int o = a.rot + (w - turned) * 8;
@@ -109,32 +118,53 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
                 load_v<T, 8>(src + o, u);
                 store_e4m3<8>(dst8 + o, u, scale);
             } else {
-                st16(dst + o, ld16(src + o));
+                stream16(dst + o, ld16(src + o));
             }
         }
+        w += dw;
+        if (w >= items) {
+            w -= items;
+            ++h;
+        }
     }
-    for (int it = threadIdx.x; it < nv; it += kThreads) {
-        const int per = a.dim / 8, h = it / per, o = (it - h * per) * 8;
-        const uint16_t* src = a.V + t * a.ldv + h * a.dim + o;
+    if (at < 0) return;
+    // v
+    h = first / per_v;
+    w = first - h * per_v;
+    const int vh = step / per_v, vw = step - vh * per_v;
+    for (; h < a.k_heads; h += vh) {
+        const uint16_t* src = a.V + t * a.ldv + h * a.dim + w * 8;
+        const int64_t to = at + h * a.head_stride + w * 8;
         if (C8) {
             float u[8];
             load_v<T, 8>(src, u);
-            store_e4m3<8>((uint8_t*)a.vc + at + h * a.head_stride + o, u, a.v_scale ? a.v_scale[h] : 1.0f);
+            store_e4m3<8>((uint8_t*)a.vc + to, u, a.v_scale ? a.v_scale[h] : 1.0f);
         } else {
-            st16((uint16_t*)a.vc + at + h * a.head_stride + o, ld16(src));
+            stream16((uint16_t*)a.vc + to, ld16(src));
+        }
+        w += vw;
+        if (w >= per_v) {
+            w -= per_v;
+            ++h;
         }
     }
 }
 
-template <typename T, int LAYOUT>
+template <typename T>
 hipError_t launch(const RopeArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.T), block(kThreads);
-    if (a.rot % 16 == 0) {
-        if (a.cache8) rope_kernel<T, LAYOUT, 8, true><<<grid, block, 0, s>>>(a);
-        else rope_kernel<T, LAYOUT, 8, false><<<grid, block, 0, s>>>(a);
+    // one workgroup per token; where that leaves CUs idle, up to 4 that share the token's items (each makes the angles)
+    const int64_t items = ((int64_t)(a.q_heads + a.k_heads) * (a.dim / 16) + (int64_t)a.k_heads * (a.dim / 8)) / kThreads;
+    const int64_t share = a.T >= 256 ? 1 : items < 1 ? 1 : items > 4 ? 4 : items;
+    const dim3 grid((unsigned)a.T, (unsigned)share), block(kThreads);
+    if (a.layout == HTS_ROPE_INTERLEAVED) {
+        if (a.cache8) rope_kernel<T, HTS_ROPE_INTERLEAVED, 4, true><<<grid, block, 0, s>>>(a);
+        else rope_kernel<T, HTS_ROPE_INTERLEAVED, 4, false><<<grid, block, 0, s>>>(a);
+    } else if (a.rot % 16 == 0) {
+        if (a.cache8) rope_kernel<T, HTS_ROPE_HALF, 8, true><<<grid, block, 0, s>>>(a);
+        else rope_kernel<T, HTS_ROPE_HALF, 8, false><<<grid, block, 0, s>>>(a);
     } else {
-        if (a.cache8) rope_kernel<T, LAYOUT, 4, true><<<grid, block, 0, s>>>(a);
-        else rope_kernel<T, LAYOUT, 4, false><<<grid, block, 0, s>>>(a);
+        if (a.cache8) rope_kernel<T, HTS_ROPE_HALF, 4, true><<<grid, block, 0, s>>>(a);
+        else rope_kernel<T, HTS_ROPE_HALF, 4, false><<<grid, block, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -142,9 +172,7 @@ hipError_t launch(const RopeArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
-    if (a.dtype == HTS_BF16)
-        return a.layout == HTS_ROPE_HALF ? launch<BF16T, HTS_ROPE_HALF>(a, s) : launch<BF16T, HTS_ROPE_INTERLEAVED>(a, s);
-    return a.layout == HTS_ROPE_HALF ? launch<F16T, HTS_ROPE_HALF>(a, s) : launch<F16T, HTS_ROPE_INTERLEAVED>(a, s);
+    return a.dtype == HTS_BF16 ? launch<BF16T>(a, s) : launch<F16T>(a, s);
 }
 
 }  // namespace hts

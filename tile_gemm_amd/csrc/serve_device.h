@@ -24,6 +24,9 @@ template <typename T> __device__ __forceinline__ u32x4 narrow8(const float* f) {
     return v;
 }
 
+// A 16-byte store that does not claim a place in the caches.
+__device__ __forceinline__ void stream16(void* p, u32x4 v) { __builtin_nontemporal_store(v, (u32x4*)p); }
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
