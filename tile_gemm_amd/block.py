@@ -9,18 +9,31 @@ back to back:
     gate = X Wg^T,  up = X Wu^T,  h = silu(gate) * up,  down = h Wd^T
 
 with every W either a packed hybrid weight (hts_gemm) or a row-major dense one
-(hts_dense_gemm, the same-library baseline).  Attention itself is not part of this library: the
-output projection reads A = q in its place, which keeps the shapes and the data dependence of
-the block.  Every call is enqueued on the current stream, so the whole step can be captured in
-one HIP graph.
+(hts_dense_gemm, the same-library baseline).  In ``forward`` the output projection reads A = q in
+place of the attention output, which keeps the shapes and the data dependence of the block.
+Every call is enqueued on the current stream, so the whole step can be captured in one HIP
+graph.
+
+``decode`` runs the whole block for one new token per request, on the steps around the products
+(``serving``): norm, q / k / v, rotary positions with k and v written to a paged cache, attention
+over the cache, o, and the residual additions with the norms around them.  A step of a model is
+one ``kv_step`` for all layers, then ``decode`` per layer:
+
+    step = kv_step(cached, ones, free_pages, table, cache.page, B, free_head=head)
+    x, r = embed(tokens), None
+    for layer in layers:
+        x, r = decode(x, r, layer, step, table, plan)
+    cached, head = step.lengths, step.head
 """
 from __future__ import annotations
 
-from typing import Dict
+import dataclasses
+from typing import Dict, Optional
 
 import torch
 
-from . import PackedWeight, dense_gemm, gemm, gemm_silu_mul, silu_mul
+from . import (KVCache, KVStep, Norm, PackedWeight, RopePlan, dense_gemm, gemm, gemm_silu_mul, paged_attn, residual_norm,
+               rope_cache, silu_mul)
 
 PROJECTIONS = ("q", "k", "v", "o", "gate", "up", "down")
 
@@ -66,3 +79,56 @@ def kept_flops(M: int, weights: Dict[str, object]) -> float:
         else:
             total += w.shape[0] * w.shape[1]
     return 2.0 * M * total
+
+
+@dataclasses.dataclass
+class Layer:
+    """A decoder block: its seven projections (packed or row-major), its norms and its cache.
+
+    input_norm and mlp_norm come before attention and the MLP; the optional post norms, gates ([hidden], or one
+    for each token) and residual_scale apply to what the two write back to the residual stream:
+    x + residual_scale * gate * post(block(norm(x)))."""
+    weights: Dict[str, object]
+    cache: KVCache
+    input_norm: Norm
+    mlp_norm: Norm
+    post_attn_norm: Optional[Norm] = None
+    post_mlp_norm: Optional[Norm] = None
+    attn_gate: Optional[torch.Tensor] = None
+    mlp_gate: Optional[torch.Tensor] = None
+    residual_scale: float = 1.0
+    window: int = 0
+    attn_scale: Optional[float] = None       # default: 1 / sqrt(head size)
+
+
+def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step: KVStep, block_table: torch.Tensor,
+           plan: RopePlan, bufs: Optional[Dict[str, torch.Tensor]] = None):
+    """One block on one new token per request: x [B, hidden], the output of the block before (its MLP, not yet
+    added) with that block's residual stream, or the embedding with residual None.  Returns (x, residual) for
+    the next block: the MLP's output and the stream it is to be added to.  The layer's post_mlp_norm, gate
+    and scale are applied here, so that the next block only adds: give the last block's pair to
+    residual_norm(x, residual, pre=final_norm).
+
+    step and block_table come from kv_step with one token added per request (its positions and slots; padding
+    rows behind the last request are carried along and change no cache entry)."""
+    w, B = layer.weights, x.shape[0]
+    if bufs is None:
+        bufs = buffers(B, w, x.dtype, x.device)
+    # r = residual + x, y = norm(r)
+    r, y = residual_norm(x, residual, pre=layer.input_norm)
+    for name in ("q", "k", "v"):
+        _linear(y, w[name], bufs[name])
+    rope_cache(bufs["q"], bufs["k"], bufs["v"], step.positions, step.slots, plan, layer.cache)
+    a = paged_attn(bufs["q"], layer.cache, block_table, step.lengths, layer.attn_scale, layer.window)
+    _linear(a, w["o"], bufs["o"])
+    r, y = residual_norm(bufs["o"], r, post=layer.post_attn_norm, pre=layer.mlp_norm, gate=layer.attn_gate,
+                         scale=layer.residual_scale, residual_out=r)
+    _linear(y, w["gate"], bufs["gate"])
+    if isinstance(w["up"], PackedWeight):
+        gemm_silu_mul(y, w["up"], bufs["gate"], out=bufs["h"])
+    else:
+        silu_mul(bufs["gate"], _linear(y, w["up"], bufs["up"]), out=bufs["h"])
+    out = _linear(bufs["h"], w["down"], bufs["down"])
+    if layer.post_mlp_norm is not None or layer.mlp_gate is not None or layer.residual_scale != 1.0:
+        out, _ = residual_norm(out, None, post=layer.post_mlp_norm, gate=layer.mlp_gate, scale=layer.residual_scale)
+    return out, r
