@@ -110,18 +110,39 @@ struct Run {
     int b;
     uint32_t off, left, per;
 };
-__device__ __forceinline__ Run find_run(const AttnArgs& a, uint32_t x, int lane) {
+// Inclusive sum over the lanes of a wave, by row shifts and row broadcasts (no LDS round trip).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+#define HTS_ROW(ctrl, rows) x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xF, false)
+    HTS_ROW(0x111, 0xF);   // row_shr:1, 2, 4, 8
+    HTS_ROW(0x112, 0xF);
+    HTS_ROW(0x114, 0xF);
+    HTS_ROW(0x118, 0xF);
+    HTS_ROW(0x142, 0xA);   // row_bcast:15 into rows 1 and 3
+    HTS_ROW(0x143, 0xC);   // row_bcast:31 into rows 2 and 3
+#undef HTS_ROW
+    return x;
+}
+
+// Lengths of the requests: in the lanes of every wave where there are at most 64, else in memory.
+struct Lengths {
+    const int32_t* p;
+    int32_t mine;
+    bool held;
+    __device__ __forceinline__ int32_t operator[](int b) const {
+        return held ? __builtin_amdgcn_readlane(mine, b) : scalar_load(p, b);
+    }
+};
+
+__device__ __forceinline__ Run find_run(const AttnArgs& a, const Lengths& lengths, uint32_t x, int lane) {
     const int each = (a.B + 63) / 64, b0 = lane * each;
     uint32_t mine = 0;
-    for (int i = 0; i < each; ++i)
-        if (b0 + i < a.B) mine += span_of(a, a.lengths[b0 + i]).steps();
-    uint32_t in = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = __shfl_up(in, o);
-        if (lane >= o) in += u;
+    if (lengths.held) {
+        if (lane < a.B) mine = span_of(a, lengths.mine).steps();
+    } else {
+        for (int i = 0; i < each; ++i)
+            if (b0 + i < a.B) mine += span_of(a, a.lengths[b0 + i]).steps();
     }
-    const uint32_t total = __builtin_amdgcn_readlane(in, 63);
+    const uint32_t in = wave_scan(mine), total = __builtin_amdgcn_readlane(in, 63);
     Run r;
     // An even share, but where that is short a longer run, down to a third as many of them: each costs a start, an
     // end and its parts (one request of 4096 tokens, 32 heads: 19.8 us with runs of 6 steps, 18.4 with 16; 8
@@ -133,8 +154,8 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, uint32_t x, int lane)
     const int owner = __builtin_ctzll(__ballot(in > pos));
     uint32_t at = __builtin_amdgcn_readlane(in - mine, owner);
     r.b = owner * each;
-    for (;;) {                                      // ends: the owner's requests hold step pos
-        const uint32_t n = span_of(a, scalar_load(a.lengths, r.b)).steps();
+    while (!lengths.held) {                          // ends: the owner's requests hold step pos
+        const uint32_t n = span_of(a, lengths[r.b]).steps();
         if (pos < at + n) break;
         at += n;
         ++r.b;
@@ -153,6 +174,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     constexpr int W = DP < 128 ? DP : 128;
     __shared__ float lds_o[kWaves][16][W + 4];
     __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
+    // q's operand: in registers, but for heads above 128 entries, where it would not fit beside K, V and O
+    constexpr bool Q_LDS = DP == 256;
+    __shared__ u32x4 lds_q[Q_LDS ? NK : 1][64];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = uniform(tid >> 6);
@@ -161,7 +185,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     const int heads = min(16, group - ht * 16), head0 = hk * group + ht * 16;
 
     Run run{(int)blockIdx.x, 0, ~0u, ~0u};
-    if (a.part_o) run = find_run(a, blockIdx.x, lane);
+    Lengths lengths{a.lengths, 0, a.part_o && a.B <= 64};
+    if (lengths.held && lane < a.B) lengths.mine = a.lengths[lane];
+    if (a.part_o) run = find_run(a, lengths, blockIdx.x, lane);
     const char* kbase = (const char*)a.kc + (int64_t)hk * a.head_stride * ES;
     const char* vbase = (const char*)a.vc + (int64_t)hk * a.head_stride * ES;
     // A half step is read through a buffer resource at its first token: a scalar base, one 32-bit offset per lane.
@@ -174,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 
     for (uint32_t slot = 2 * blockIdx.x; run.left; slot |= 1) {   // one request, or the part of it in this run
     const int b = run.b;
-    const Span sp = span_of(a, scalar_load(a.lengths, b));
+    const Span sp = span_of(a, lengths[b]);
     const uint32_t steps = sp.steps(), n_steps = min(steps - run.off, run.left);
     const bool whole_request = n_steps == steps;
     const uint32_t first = sp.begin + 32 * run.off;
@@ -189,14 +215,20 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         run.left = 0;
     }
 
-    u32x4 q[NK];
+    u32x4 q[Q_LDS ? 1 : NK];
     {
         const uint16_t* row = a.Q + b * a.ldq + (int64_t)(head0 + c) * a.dim;
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            q[k] = u32x4{0, 0, 0, 0};
+        const auto load_q = [&](int k) {
             const int d = 32 * k + 8 * g;
-            if (c < heads && (FULL || d < a.dim)) q[k] = ld16(row + d);
+            return c < heads && (FULL || d < a.dim) ? ld16(row + d) : u32x4{0, 0, 0, 0};
+        };
+        if constexpr (Q_LDS) {
+#pragma unroll
+            for (int k = 0; k < NK / kWaves; ++k) lds_q[wave + kWaves * k][lane] = load_q(wave + kWaves * k);
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int k = 0; k < NK; ++k) q[k] = load_q(k);
         }
     }
     const int32_t* table = a.table + b * a.ldt;
@@ -227,7 +259,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             const auto from = resource(kbase, h[j].off);
 #pragma unroll
             for (int k = 0; k < NK; ++k)
-                kr[j][k].load(from, FULL || 32 * k + 8 * g < a.dim ? k_lane + 32 * k * ES : kBufferEnd, 0);
+                kr[j][k].load(from, FULL || 32 * k + 8 * g < a.dim ? k_lane : kBufferEnd, 32 * k * ES);
         }
     };
     const auto load_v = [&](const Half* h) {
@@ -238,8 +270,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
-                    vr[n][4 * j + i].load(from, FULL || 128 * n + VEC * c < a.dim ? v_lane + 128 * n * ES : kBufferEnd,
-                                          i * v_step);
+                    vr[n][4 * j + i].load(from, FULL || 128 * n + VEC * c < a.dim ? v_lane : kBufferEnd,
+                                          i * v_step + 128 * n * ES);
         }
     };
 
@@ -271,7 +303,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             for (int k = 0; k < NK; ++k) {
                 const u32x4 x = {kr[j][k].template pair<T>(0), kr[j][k].template pair<T>(1),
                                  kr[j][k].template pair<T>(2), kr[j][k].template pair<T>(3)};
-                s[j] = mfma_dense<T>(x, q[k], s[j]);
+                s[j] = mfma_dense<T>(x, Q_LDS ? lds_q[k][lane] : q[Q_LDS ? 0 : k], s[j]);
             }
         }
         if (MORE) {
@@ -416,54 +448,61 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 }
 
 // Join the parts of a split request: one workgroup per request and query head.  Row r of dim / 4 lanes takes
-// parts r, r + rows, ... (their loads do not wait for the weights), and the rows' sums are added in order.
-constexpr int kJoinThreads = 128, kJoinParts = 4;
+// parts r, r + rows, ..., 8 at a time (the first ones' loads do not wait for the weights); the rows' sums are added
+// in order.
+constexpr int kJoinThreads = 256, kJoinParts = 8;
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
     __shared__ f32x4 lds[kJoinThreads];
     __shared__ float lds_m[kJoinThreads / 64], lds_l[kJoinThreads / 64];
-    const int b = blockIdx.x, h = blockIdx.y;
+    const int b = blockIdx.x, h = blockIdx.y, threads = blockDim.x, waves = threads / 64;
     const uint2 plan = a.plan[b];
-    if (plan.y <= 1) return;
+    const int parts = (int)plan.y;
+    if (parts <= 1) return;
     const int group = a.q_heads / a.k_heads, hk = h / group, gh = h - hk * group;
     const int y = hk * a.head_tiles + gh / 16, all_rows = a.k_heads * a.head_tiles;
     const int tid = threadIdx.x, lane = tid & 63;
     // the first part's slot, then the first slot of each run after it
-    const auto part = [&](uint32_t i) {
+    const auto part = [&](int i) {
         return ((int64_t)(i ? 2 * (plan.x / 2 + i) : plan.x) * all_rows + y) * a.tile_heads + (gh & 15);
     };
-    const int quads = a.dim / 4, rows = kJoinThreads / quads, row = tid / quads, d = (tid - row * quads) * 4;
-    const bool on = row < rows;
+    const int quads = a.dim / 4, rows = threads / quads, row = tid / quads, d = (tid - row * quads) * 4;
     f32x4 x[kJoinParts];
-    float2 ml[kJoinParts];
+    float m[kJoinParts];
+    const auto load = [&](int base) {
 #pragma unroll
-    for (int k = 0; k < kJoinParts; ++k) {
-        const uint32_t i = row + k * rows;
-        x[k] = f32x4{0, 0, 0, 0};
-        ml[k] = float2{-INFINITY, 0.0f};
-        if (on && i < plan.y) {
-            x[k] = *reinterpret_cast<const f32x4*>(a.part_o + part(i) * a.dim + d);
-            ml[k] = a.part_ml[part(i)];
+        for (int k = 0; k < kJoinParts; ++k) {
+            const int i = base + k * rows;
+            x[k] = f32x4{0, 0, 0, 0};
+            m[k] = -INFINITY;
+            if (row < rows && i < parts) {
+                x[k] = *reinterpret_cast<const f32x4*>(a.part_o + part(i) * a.dim + d);
+                m[k] = a.part_ml[part(i)].x;
+            }
         }
-    }
-    float top = -INFINITY;
-    for (uint32_t i = tid; i < plan.y; i += kJoinThreads) top = fmaxf(top, a.part_ml[part(i)].x);
+    };
+    load(row);
+    float2 ml = {-INFINITY, 0.0f};       // this thread's part of the maximum and the sum
+    if (tid < parts) ml = a.part_ml[part(tid)];
+    float top = ml.x;
+    for (int i = tid + threads; i < parts; i += threads) top = fmaxf(top, a.part_ml[part(i)].x);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
     if (lane == 0) lds_m[tid >> 6] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, lds_m[w]);
-    const auto weight = [&](float m) { return m == -INFINITY ? 0.0f : exp2f(m - top); };
+    for (int w = 0; w < waves; ++w) top = fmaxf(top, lds_m[w]);
+    const auto weight = [&](float v) { return v == -INFINITY ? 0.0f : exp2f(v - top); };
     f32x4 sum = {0, 0, 0, 0};
+    for (int base = row;;) {
 #pragma unroll
-    for (int k = 0; k < kJoinParts; ++k) sum += x[k] * weight(ml[k].x);
-    if (on)
-        for (uint32_t i = row + kJoinParts * rows; i < plan.y; i += rows)
-            sum += *reinterpret_cast<const f32x4*>(a.part_o + part(i) * a.dim + d) * weight(a.part_ml[part(i)].x);
+        for (int k = 0; k < kJoinParts; ++k) sum += x[k] * weight(m[k]);
+        base += kJoinParts * rows;
+        if (row >= rows || base >= parts) break;
+        load(base);
+    }
     lds[tid] = sum;
-    float l = 0.0f;
-    for (uint32_t i = tid; i < plan.y; i += kJoinThreads) {
+    float l = ml.y * weight(ml.x);
+    for (int i = tid + threads; i < parts; i += threads) {
         const float2 v = a.part_ml[part(i)];
         l += v.y * weight(v.x);
     }
@@ -472,8 +511,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
     __syncthreads();
     if (row) return;
     l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 64; ++w) l += lds_l[w];
+    for (int w = 0; w < waves; ++w) l += lds_l[w];
     sum = f32x4{0, 0, 0, 0};
     for (int r = 0; r < rows; ++r) sum += lds[r * quads + tid];
     const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[hk] : 1.0f) / l;
@@ -494,7 +532,9 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
     else attn_kernel<T, C8, 256, false><<<grid, block, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part_o) return e;
-    join_kernel<T><<<dim3((unsigned)a.B, (unsigned)a.q_heads), dim3(kJoinThreads), 0, s>>>(a);
+    // few joins have many parts each: four waves; many have few: two
+    const unsigned threads = (int64_t)a.B * a.q_heads <= 512 ? 256 : 128;
+    join_kernel<T><<<dim3((unsigned)a.B, (unsigned)a.q_heads), dim3(threads), 0, s>>>(a);
     return hipGetLastError();
 }
 

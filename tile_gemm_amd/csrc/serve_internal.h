@@ -71,6 +71,9 @@ struct AttnArgs {
 };
 // Requests whose runs every wave finds by one scan; more run unsplit.
 constexpr int64_t kMaxSplitRequests = 4096;
+// Where no request can be longer, each is one workgroup's (51 requests up to 455 tokens, 21/3 heads of 192: 17 us
+// against 32 in runs with a join).
+constexpr int kAttnWholeTokens = 512;
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
 constexpr int64_t kMaxNormWidth = 32768;
