@@ -599,3 +599,97 @@ def test_helpers_refuse():
         with pytest.raises(hts.HTSError):
             f()
             say(f"refusal {i} did not happen")
+
+
+# ---- wide batches, bounds --------------------------------------------------
+
+@pytest.mark.parametrize("B,hq,hk,dim,top", [(130, 2, 1, 64, 1500),      # lengths over several lanes' reach
+                                             (64, 4, 2, 128, 700), (65, 3, 3, 8, 900),
+                                             (700, 8, 4, 32, 600),
+                                             (4500, 2, 2, 16, 560),      # more requests than are split
+                                             (2, 800, 800, 8, 1100)])    # more heads than the chip holds at once
+def test_paged_attn_of_many_requests(B, hq, hk, dim, top):
+    g = np.random.default_rng(B)
+    page, pages = 16, 200
+    width = -(-top // page)
+    c = hts.kv_cache(pages, page, hk, dim, torch.bfloat16, DEV)
+    for x in (c.k, c.v):
+        x.copy_(torch.randn(x.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(B)).bfloat16())
+    lengths = g.integers(0, top + 1, B) * (g.random(B) < 0.8)
+    lengths[-1] = top
+    table = g.integers(0, pages, (B, width))       # pages are shared: reading them does no harm
+    q = normal(g, (B, hq * dim), "bf16")
+    lse = torch.empty((B, hq), device=DEV)
+    say(f"[attn] B={B} {hq}/{hk} dim={dim} lengths to {top}")
+    out = hts.paged_attn(q, c, i32(table), i32(lengths), lse=lse)
+    some = np.unique(np.concatenate([g.integers(0, B, 12), [0, B - 1]]))
+    heads = np.unique(np.concatenate([g.integers(0, hq, 4), [0, hq - 1]]))
+    kv = heads // (hq // hk)
+    k, v = f64(c.k[:, :, kv]), f64(c.v[:, :, kv])
+    qs = f64(q).reshape(B, hq, dim)[some][:, heads]
+    want, wl, err, el = ref.attn(qs, k, v, table[some], lengths[some], page, dim ** -0.5, 0, len(heads))
+    got = f64(out).reshape(B, hq, dim)[some][:, heads]
+    assert np.all(np.abs(got - want) <= ref.EPS["bf16"] / 2 * np.abs(want) + err + ref.TINY["bf16"])
+    gl = f64(lse)[some][:, heads]
+    live = ~np.isinf(wl)
+    assert np.array_equal(gl[~live], wl[~live]) and np.all(np.abs(gl - wl)[live] <= el[live])
+
+
+def test_steps_write_only_their_outputs():
+    # canary values around the attention's output, sums and workspace, and around the page step's outputs
+    pad = 512
+    lengths = [3000, 17, 0, 1200]
+    q, c, table, width = _attn_case(128, 12, 2, 16, "token", "same", lengths, "bf16", 21)
+    need = c.workspace_bytes(4, 12, width, 0)
+    assert need > 0
+    ws = torch.full((need + 2 * pad,), 0x5A, dtype=torch.uint8, device=DEV)
+    o = torch.full((4 * 12 * 128 + 2 * pad,), 9.0, dtype=torch.bfloat16, device=DEV)
+    ls = torch.full((48 + 2 * pad,), 9.0, device=DEV)
+    lse = ls[pad:-pad].view(4, 12)
+    out = hts.paged_attn(q, c, i32(table)[:, :width], i32(lengths), out=o[pad:-pad].view(4, -1), lse=lse,
+                         workspace=ws[pad:-pad])
+    assert torch.equal(out, hts.paged_attn(q, c, i32(table)[:, :width], i32(lengths)))
+    assert torch.all(ws[:pad] == 0x5A) and torch.all(ws[-pad:] == 0x5A)
+    for t in (o, ls):
+        assert torch.all(t[:pad] == 9.0) and torch.all(t[-pad:] == 9.0)
+    B, T = 70, 200
+    cached, added, free, tab, _ = _step_case(B, 16, 9, 5, "mixed")
+    bufs = {n: torch.full((s + 2 * pad,), -77, dtype=d, device=DEV)
+            for n, s, d in (("lengths", B, torch.int32), ("starts", B + 1, torch.int32), ("slots", T, torch.int64),
+                            ("positions", T, torch.int32), ("head", 1, torch.int32))}
+    st = hts.KVStep(**{n: b[pad:-pad] for n, b in bufs.items()})
+    hts.kv_step(i32(cached), i32(added), i32(free), i32(tab)[:, :9], 16, T, out=st)
+    for n, b in bufs.items():
+        assert torch.all(b[:pad] == -77) and torch.all(b[-pad:] == -77), n
+        assert torch.all(b[pad:-pad] != -77), n
+
+
+def test_debug_mode_refuses_short_buffers(monkeypatch):
+    # HTS_DEBUG=1 finds a buffer shorter than the call needs before anything is enqueued, and changes no result
+    from test_gpu_debug import DeviceBuffer
+    lengths = [900, 3]
+    q, c, table, width = _attn_case(128, 8, 2, 16, "token", "same", lengths, "bf16", 31)
+    t, n = i32(table)[:, :width], i32(lengths)
+    plain = hts.paged_attn(q, c, t, n)
+    x = normal(np.random.default_rng(0), (64, 4096), "bf16")
+    r0, y0 = hts.residual_norm(x, x, pre=hts.Norm("rms"))
+    monkeypatch.setenv("HTS_DEBUG", "1")
+    assert torch.equal(hts.paged_attn(q, c, t, n), plain)
+    r1, y1 = hts.residual_norm(x, x, pre=hts.Norm("rms"))
+    assert torch.equal(r0, r1) and torch.equal(y0, y1)
+    short = DeviceBuffer(64 * 4096)               # half of a 64 x 4096 matrix of 16-bit values
+    big = torch.empty((2048, 16, 2, 128), dtype=torch.bfloat16, device=DEV)
+    import ctypes
+    L = hts.lib()
+    try:
+        d = hts.hts_norm_desc(1, 1, 0, 1, 1e-6, 1e-6, 1.0, 0)
+        assert L.hts_residual_norm(ctypes.byref(d), 64, 4096, x.data_ptr(), 4096, None, None, None, 0, None, 0, None, None,
+                                   None, 0, short.ptr.value, 4096, None) == 3
+        assert b"Y needs" in L.hts_last_error()
+        kv = hts.KVCache(big, big.clone())
+        assert L.hts_paged_attn(1, 2, 8, ctypes.byref(kv.desc), q.data_ptr(), 1024, short.ptr.value, kv.v.data_ptr(), None,
+                                None, t.data_ptr(), t.stride(0), width, n.data_ptr(), 0.1, 0, plain.data_ptr(), 1024, None,
+                                None, 0, None) == 3
+        assert b"k_cache needs" in L.hts_last_error()
+    finally:
+        short.free()
