@@ -146,8 +146,10 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, const Lengths& length
     Run r;
     // An even share, but where that is short a longer run, down to a third as many of them: each costs a start, an
     // end and its parts (one request of 4096 tokens, 32 heads: 19.8 us with runs of 6 steps, 18.4 with 16; 8
-    // requests up to 1024, 32/8 heads: 13.9 with 8, 16.1 with 16).
-    r.per = max((total + gridDim.x - 1) / gridDim.x, min(max(3 * total / a.target, 8u), 16u));
+    // requests up to 1024, 32/8 heads: 13.9 with 8, 16.1 with 16) -- and not longer for that than the requests are, which
+    // cost as much each.
+    const uint32_t few = min(min(max(3 * total / a.target, 8u), 16u), (total + a.B - 1) / a.B);
+    r.per = max((total + gridDim.x - 1) / gridDim.x, few);
     const uint32_t pos = x * r.per;
     r.left = pos < total ? min(r.per, total - pos) : 0;
     if (!r.left) return r;
@@ -195,6 +197,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     const uint32_t k_lane = ((uint32_t)c * (uint32_t)a.token_stride + 8 * g) * ES;
     const uint32_t v_lane = ((uint32_t)(4 * g) * (uint32_t)a.token_stride + VEC * c) * ES;
     const uint32_t v_step = (uint32_t)a.token_stride * ES, page_mask = (1u << a.page_shift) - 1;
+    const uint32_t pages = (uint32_t)a.pages;   // below 2^31: an id below 0 is not below it
+    const int64_t page_bytes = a.page_stride * ES;
     const float s_scale = a.scale * kLog2e * (C8 && a.k_scale ? a.k_scale[hk] : 1.0f);
     const float v_scale = C8 && a.v_scale ? a.v_scale[hk] : 1.0f;
 
@@ -232,6 +236,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         }
     }
     const int32_t* table = a.table + b * a.ldt;
+    const uint32_t last_page = (a.cap - 1) >> a.page_shift;   // ids past it are asked for, but never used
+    const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
 
     // the two 16-token halves of the step at t: the page's id (requested a step ahead), then the byte offset of
     // the half's first token and whether a page holds it
@@ -239,12 +245,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         int64_t off;
         bool ok;
     };
-    const uint32_t last_page = (a.cap - 1) >> a.page_shift;   // ids past it are asked for, but never used
-    const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
     const auto half = [&](uint32_t t, int32_t id) {
         Half h;
-        h.ok = id >= 0 && id < a.pages;
-        h.off = ((h.ok ? id : 0) * a.page_stride + (int64_t)(t & page_mask) * a.token_stride) * ES;
+        h.ok = (uint32_t)id < pages;
+        h.off = (h.ok ? id : 0) * page_bytes + (uint64_t)(t & page_mask) * v_step;
         return h;
     };
     Raw<C8, 8> kr[2][NK];
