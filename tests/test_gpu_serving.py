@@ -416,6 +416,33 @@ def test_paged_attn_extreme_scores():
     assert bool(torch.isnan(out[0, 3])) and int(torch.isnan(out).sum()) == 1
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_paged_attn_small_weights_add_up(dtype):
+    # one token of weight 1 and value 0, and 100000 of weight e^-18 (2^-26) and value 1: together 1.5e-3
+    page, n = 64, 100001
+    pages = -(-n // page)
+    c = hts.kv_cache(pages, page, 1, 64, TORCH[dtype], DEV)
+    c.k[..., 0] = -18.0
+    c.v.fill_(1.0)
+    for first in (0, 70000):                    # the large weight first, and late (in another run)
+        c.k[first // page, first % page, 0, 0] = 0.0
+        c.v[first // page, first % page] = 0.0
+        q = torch.zeros((1, 2 * 64), dtype=TORCH[dtype], device=DEV)
+        q[0, 0] = 1.0
+        q[0, 64] = 0.5                           # the second head: weights e^-9
+        lse = torch.empty((1, 2), device=DEV)
+        out = hts.paged_attn(q, c, torch.arange(pages, dtype=torch.int32, device=DEV)[None], i32([n]), scale=1.0, lse=lse)
+        got = f64(out)[0].reshape(2, 64)
+        for h, w in enumerate((np.exp(-18.0), np.exp(-9.0))):
+            want = (n - 1) * w / (1 + (n - 1) * w)
+            # half a step of the type, the weights' 2^-16, and 100000 additions in 32 bits over 96 lanes and more
+            tol = (ref.EPS[dtype] / 2 + 2.0 ** -16 + n / 96 * 2.0 ** -24) * want
+            assert np.all(np.abs(got[h] - want) <= tol), (first, h, got[h][:2], want)
+            assert abs(float(lse[0, h]) - np.log(1 + (n - 1) * w)) <= 1e-4
+        c.k[first // page, first % page, 0, 0] = -18.0
+        c.v[first // page, first % page] = 1.0
+
+
 @pytest.mark.parametrize("lengths", [[100, 3], [9000, 70, 0]])
 def test_paged_attn_in_a_graph(lengths):
     # captured once at one set of lengths, replayed at others with eager work in between

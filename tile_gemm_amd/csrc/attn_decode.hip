@@ -15,7 +15,7 @@
 //                 transposes them in registers (one byte permute per two values).
 // So the maximum, the sum and the accumulators of a head stay in the lanes of that head, and no
 // value crosses lanes in the loop but the maximum -- and that only when a score passes the last
-// reference by 2^8, which rescales; below that the weights stay under 256 and nothing is lost.
+// reference by 2^8, which rescales; below that the weights stay in range and nothing is lost.
 // Weights are split into two 16-bit parts (their sum holds 16 bits and more), so that the product
 // with V rounds them no further than 2^-16: the matrix cores are idle most of the time.
 // K's registers are reloaded for the next step as soon as the scores are out, V's as soon as O is.
@@ -36,6 +36,9 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+// Weights are 2^(s - m + 7): at most 2^15, since m is at least the maximum less 8, which binary16 holds, and still
+// above its smallest value, 2^-24, where they are 2^-31 of the largest (many such weights add up in a long context).
+constexpr float kShift = 7.0f;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -342,7 +345,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             top = fmaxf(top, m);
             const float f = exp2f(m - (top == -INFINITY ? 0.0f : top));
             m = top;
-            ref = top == -INFINITY ? 0.0f : top;
+            ref = top == -INFINITY ? 0.0f : top - kShift;
             l *= f;
 #pragma unroll
             for (int n = 0; n < NH; ++n)
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
                 *reinterpret_cast<uint2*>(out) = uint2{narrow<T>(sum[0] * inv) | (narrow<T>(sum[1] * inv) << 16),
                                                        narrow<T>(sum[2] * inv) | (narrow<T>(sum[3] * inv) << 16)};
                 if (at == 0 && a.lse)
-                    a.lse[(int64_t)b * a.q_heads + head0 + h] = den == 0.0f ? -INFINITY : (top + log2f(den)) * kLn2;
+                    a.lse[(int64_t)b * a.q_heads + head0 + h] = den == 0.0f ? -INFINITY : (top - kShift + log2f(den)) * kLn2;
             }
         }
     }
@@ -473,7 +476,7 @@ __device__ __forceinline__ void write_joined(const AttnArgs& a, int b, int h, in
     *reinterpret_cast<uint2*>(a.O + b * a.ldo + (int64_t)h * a.dim + d) =
         uint2{narrow<T>(sum[0] * inv) | (narrow<T>(sum[1] * inv) << 16),
               narrow<T>(sum[2] * inv) | (narrow<T>(sum[3] * inv) << 16)};
-    if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + h] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + h] = l == 0.0f ? -INFINITY : (top - kShift + log2f(l)) * kLn2;
 }
 
 // Join of many heads of few parts: a thread takes four entries of one head through all its parts, in order, with a
