@@ -198,3 +198,19 @@ def test_padding_rows_change_nothing():
     assert torch.equal(a, b[:, :4]) and torch.equal(ta, tb[:4])
     for k, layer in zip(k0, model.layers):
         assert torch.equal(k, layer.cache.k)
+
+
+def test_block_refuses_shapes_that_do_not_fit():
+    model = Model(torch.bfloat16, seed=6)
+    layer, st = model.layers[0], hts.KVStep.buffers(2, 2, DEV)
+    table = torch.zeros((2, 4), dtype=torch.int32, device=DEV)
+    x = torch.zeros((2, HID), dtype=torch.bfloat16, device=DEV)
+    for change in (dict(k=layer.weights["q"]), dict(down=layer.weights["up"]), dict(o=layer.weights["k"]),
+                   dict(v=hts.unpack(layer.weights["v"]).half())):
+        with pytest.raises(hts.HTSError):
+            block.Layer({**layer.weights, **change}, layer.cache, layer.input_norm, layer.mlp_norm)
+    with pytest.raises(hts.HTSError):
+        block.Layer({n: w for n, w in layer.weights.items() if n != "up"}, layer.cache, layer.input_norm, layer.mlp_norm)
+    for bad in (x.half(), x[:1], x[:, :256]):
+        with pytest.raises(hts.HTSError):
+            block.decode(bad, None, layer, st, table, model.plan)

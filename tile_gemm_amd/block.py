@@ -32,7 +32,7 @@ from typing import Dict, Optional
 
 import torch
 
-from . import (KVCache, KVStep, Norm, PackedWeight, RopePlan, dense_gemm, gemm, gemm_silu_mul, paged_attn, residual_norm,
+from . import (HTSError, KVCache, KVStep, Norm, PackedWeight, RopePlan, dense_gemm, gemm, gemm_silu_mul, paged_attn, residual_norm,
                rope_cache, silu_mul)
 
 PROJECTIONS = ("q", "k", "v", "o", "gate", "up", "down")
@@ -100,6 +100,23 @@ class Layer:
     window: int = 0
     attn_scale: Optional[float] = None       # default: 1 / sqrt(head size)
 
+    def __post_init__(self):
+        # The products take any input that their leading dimension lets through: the block's own shapes are held here.
+        shape = {n: ((w.N, w.K) if isinstance(w, PackedWeight) else tuple(w.shape), w.dtype)
+                 for n, w in self.weights.items()}
+        if sorted(shape) != sorted(PROJECTIONS):
+            raise HTSError(1, f"a block has the projections {', '.join(PROJECTIONS)}")
+        (nq, hidden), dt = shape["q"]
+        self.hidden = hidden
+        nk, inner = self.cache.heads * self.cache.dim, shape["gate"][0][0]
+        want = dict(q=(nq, hidden), k=(nk, hidden), v=(nk, hidden), o=(hidden, nq), gate=(inner, hidden),
+                    up=(inner, hidden), down=(hidden, inner))
+        for n, (got, t) in shape.items():
+            if t != dt or t not in (torch.float16, torch.bfloat16):
+                raise HTSError(2, f"{n} has type {t}: a block's weights share one 16-bit type")
+            if got != want[n]:
+                raise HTSError(3, f"{n} is {got[0]} x {got[1]}, the block's other shapes ask for {want[n][0]} x {want[n][1]}")
+
 
 def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step: KVStep, block_table: torch.Tensor,
            plan: RopePlan, bufs: Optional[Dict[str, torch.Tensor]] = None):
@@ -112,6 +129,12 @@ def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step
     step and block_table come from kv_step with one token added per request (its positions and slots; padding
     rows behind the last request are carried along and change no cache entry)."""
     w, B = layer.weights, x.shape[0]
+    if x.dim() != 2 or x.shape[1] != layer.hidden:
+        raise HTSError(3, f"x has shape {tuple(x.shape)}, the block's hidden size is {layer.hidden}")
+    if x.dtype != w["q"].dtype:
+        raise HTSError(2, f"x has type {x.dtype}, the block's weights {w['q'].dtype}")
+    if step.positions.numel() != B or step.lengths.numel() != B:
+        raise HTSError(3, f"x has {B} rows, the step {step.lengths.numel()} requests and {step.positions.numel()} tokens")
     if bufs is None:
         bufs = buffers(B, w, x.dtype, x.device)
     # r = residual + x, y = norm(r)

@@ -399,6 +399,8 @@ def residual_norm(block: Optional[torch.Tensor], residual: Optional[torch.Tensor
     (M, N), dev = ref.shape, _gpu(ref, "block" if ref is block else "residual")
     post, pre = post or _NO_NORM, pre or _NO_NORM
     dt = block.dtype if block is not None else out.dtype if out is not None else out_dtype or residual.dtype
+    if out_dtype is not None and out_dtype != dt:
+        _bad(f"out_dtype {out_dtype}: y has the type of block and out, {dt}", 2)
     if dt not in _16:
         _bad(f"block and out of type {dt}: float16 or bfloat16 are taken", 2)
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else dt
@@ -424,9 +426,14 @@ def residual_norm(block: Optional[torch.Tensor], residual: Optional[torch.Tensor
             ldg = _lead(gate, "gate", M, N, dt, dev)
     if residual is not None:
         at_r, ldr = residual.data_ptr(), _lead(residual, "residual", M, N, rdt, dev)
-    w = [None if t is None else _vec(t, name, N, dt, dev)
-         for t, name in ((post.weight, "post weight"), (post.bias, "post bias"), (pre.weight, "pre weight"),
-                         (pre.bias, "pre bias"))]
+    w, what = post.weight, "a norm's weight or bias"
+    post_w = None if w is None else _vec(w, what, N, dt, dev)
+    w = post.bias
+    post_b = None if w is None else _vec(w, what, N, dt, dev)
+    w = pre.weight
+    pre_w = None if w is None else _vec(w, what, N, dt, dev)
+    w = pre.bias
+    pre_b = None if w is None else _vec(w, what, N, dt, dev)
     with _scope(dev, stream):
         at_ro = at_y = None
         ldro = ldy = N
@@ -444,6 +451,6 @@ def residual_norm(block: Optional[torch.Tensor], residual: Optional[torch.Tensor
             at_ro = residual_out.data_ptr()
         if out is not None:
             at_y = out.data_ptr()
-        _c._check(_c.lib().hts_residual_norm(desc, M, N, at_block, ldb, w[0], w[1], at_gate, ldg, at_r, ldr, w[2], w[3],
-                                             at_ro, ldro, at_y, ldy, _c._current_stream(dev)))
+        _c._check(_c.lib().hts_residual_norm(desc, M, N, at_block, ldb, post_w, post_b, at_gate, ldg, at_r, ldr, pre_w,
+                                             pre_b, at_ro, ldro, at_y, ldy, _c._current_stream(dev)))
     return residual_out, out
