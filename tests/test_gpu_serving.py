@@ -330,6 +330,9 @@ def test_paged_attn(dim, hq, hk, page, order, cache, window, lengths, dtype):
     again = hts.paged_attn(q, c, t, i32(lengths), scale=scale, window=window)
     assert torch.equal(again, out)
     q2 = q.clone()
+    hts.paged_attn(q2, c, t, i32(lengths), scale=scale, window=window, out=q2)
+    assert torch.equal(q2, out)
+    q2 = q.clone()
     small = torch.empty(16, dtype=torch.uint8, device=DEV)
     hts.paged_attn(q2, c, t, i32(lengths), scale=scale, window=window, out=q2, workspace=small)
     _check_attn(q, c, table, width, lengths, hq, window, scale, q2, None, dtype)

@@ -169,8 +169,9 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, const Lengths& length
     return r;
 }
 
-// DP: the head size rounded up to 64, 128 or 256; FULL: it is the head size.
-template <typename T, bool C8, int DP, bool FULL>
+// DP: the head size rounded up to 64, 128 or 256; FULL: it is the head size.  SPLIT: the workgroup takes a run of steps,
+// else request blockIdx.x.
+template <typename T, bool C8, int DP, bool FULL, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(AttnArgs a) {
     constexpr int NK = DP / 32;                 // 32-entry steps of q.k
     constexpr int VEC = DP == 64 ? 4 : 8;       // entries of V a lane holds per token and half
@@ -190,9 +191,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     const int heads = min(16, group - ht * 16), head0 = hk * group + ht * 16;
 
     Run run{(int)blockIdx.x, 0, ~0u, ~0u};
-    Lengths lengths{a.lengths, 0, a.part_o && a.B <= 64};
+    Lengths lengths{a.lengths, 0, SPLIT && a.B <= 64};
     if (lengths.held && lane < a.B) lengths.mine = a.lengths[lane];
-    if (a.part_o) run = find_run(a, lengths, blockIdx.x, lane);
+    if (SPLIT) run = find_run(a, lengths, blockIdx.x, lane);
     const char* kbase = (const char*)a.kc + (int64_t)hk * a.head_stride * ES;
     const char* vbase = (const char*)a.vc + (int64_t)hk * a.head_stride * ES;
     // A half step is read through a buffer resource at its first token: a scalar base, one 32-bit offset per lane.
@@ -207,12 +208,22 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 
     for (uint32_t slot = 2 * blockIdx.x; run.left; slot |= 1) {   // one request, or the part of it in this run
     const int b = run.b;
+    const int32_t* table = a.table + b * a.ldt;
+    const uint32_t last_page = (a.cap - 1) >> a.page_shift;   // ids past it are asked for, but never used
+    const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
+    // a request of its own starts at its first token, unless a window cuts it: its first pages are asked for together
+    // with its length
+    int32_t early[4];
+    const bool known = !SPLIT && !a.window;
+    if (known)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) early[i] = page_id(32 * wave + 16 * (i & 1) + 32 * kWaves * (i >> 1));
     const Span sp = span_of(a, lengths[b]);
     const uint32_t steps = sp.steps(), n_steps = min(steps - run.off, run.left);
     const bool whole_request = n_steps == steps;
     const uint32_t first = sp.begin + 32 * run.off;
     const uint32_t last = min(sp.len, first + 32 * n_steps);
-    if (a.part_o) {
+    if (SPLIT) {
         if (run.off == 0 && y == 0 && tid == 0)
             a.plan[b] = uint2{slot, 1 + (steps - n_steps + run.per - 1) / run.per};
         run.left -= n_steps;
@@ -238,10 +249,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             for (int k = 0; k < NK; ++k) q[k] = load_q(k);
         }
     }
-    const int32_t* table = a.table + b * a.ldt;
-    const uint32_t last_page = (a.cap - 1) >> a.page_shift;   // ids past it are asked for, but never used
-    const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
-
     // the two 16-token halves of the step at t: the page's id (requested a step ahead), then the byte offset of
     // the half's first token and whether a page holds it
     struct Half {
@@ -390,39 +397,35 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         }
     };
     if (t < last) {
-        now[0] = half(t, page_id(t));
-        now[1] = half(t + 16, page_id(t + 16));
-        ahead[0] = page_id(t + 32 * kWaves);
-        ahead[1] = page_id(t + 32 * kWaves + 16);
+        now[0] = half(t, known ? early[0] : page_id(t));
+        now[1] = half(t + 16, known ? early[1] : page_id(t + 16));
+        ahead[0] = known ? early[2] : page_id(t + 32 * kWaves);
+        ahead[1] = known ? early[3] : page_id(t + 32 * kWaves + 16);
         load_k(now);
         load_v(now);
         while (last - t > 32 * kWaves) step(std::true_type());
         step(std::false_type());
     }
 
-    // the four waves' parts of each head, in order
+    // the four waves' parts of each head, weighted by their maxima and summed in order
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     if (g == 0) {
         lds_m[wave][c] = m;
         lds_l[wave][c] = l;
     }
-    __syncthreads();
-    float all = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) all = fmaxf(all, lds_m[w][c]);
-    const float f = m == -INFINITY ? 0.0f : exp2f(m - all);
     const int64_t part = ((int64_t)slot * gridDim.y + y) * a.tile_heads;
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
         if (n) __syncthreads();
         // lane (c, g) holds 4 VEC entries of head c in a row, from 4 VEC g on in its half
+        if (c < heads)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; j += 4)
-                *reinterpret_cast<f32x4*>(&lds_o[wave][c][4 * VEC * g + VEC * i + j]) =
-                    f32x4{o[n][j][i] * f, o[n][j + 1][i] * f, o[n][j + 2][i] * f, o[n][j + 3][i] * f};
+                for (int j = 0; j < VEC; j += 4)
+                    *reinterpret_cast<f32x4*>(&lds_o[wave][c][4 * VEC * g + VEC * i + j]) =
+                        f32x4{o[n][j][i], o[n][j + 1][i], o[n][j + 2][i], o[n][j + 3][i]};
         __syncthreads();
         for (int it = tid; it < heads * (W / 4); it += 64 * kWaves) {
             const int h = it / (W / 4), d = (it & (W / 4 - 1)) * 4, at = 128 * n + d;
@@ -430,13 +433,13 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
             f32x4 sum = {0, 0, 0, 0};
             float top = -INFINITY, den = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                sum += *reinterpret_cast<const f32x4*>(&lds_o[w][h][d]);
-                top = fmaxf(top, lds_m[w][h]);
-            }
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, lds_m[w][h]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                den += lds_m[w][h] == -INFINITY ? 0.0f : lds_l[w][h] * exp2f(lds_m[w][h] - top);
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = lds_m[w][h] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lds_m[w][h] - top);
+                sum += *reinterpret_cast<const f32x4*>(&lds_o[w][h][d]) * f;
+                den = fmaf(lds_l[w][h], f, den);
+            }
             if (!whole_request) {
                 *reinterpret_cast<f32x4*>(a.part_o + (part + h) * a.dim + at) = sum;
                 if (at == 0) a.part_ml[part + h] = float2{top, den};
@@ -587,15 +590,21 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
     write_joined<T>(a, b, h, d, sum, l, top);
 }
 
+template <typename T, bool C8, bool SPLIT>
+void launch_runs(const AttnArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(SPLIT ? a.runs : a.B), (unsigned)(a.k_heads * a.head_tiles)), block(64 * kWaves);
+    if (a.dim == 64) attn_kernel<T, C8, 64, true, SPLIT><<<grid, block, 0, s>>>(a);
+    else if (a.dim < 64) attn_kernel<T, C8, 64, false, SPLIT><<<grid, block, 0, s>>>(a);
+    else if (a.dim == 128) attn_kernel<T, C8, 128, true, SPLIT><<<grid, block, 0, s>>>(a);
+    else if (a.dim < 128) attn_kernel<T, C8, 128, false, SPLIT><<<grid, block, 0, s>>>(a);
+    else if (a.dim == 256) attn_kernel<T, C8, 256, true, SPLIT><<<grid, block, 0, s>>>(a);
+    else attn_kernel<T, C8, 256, false, SPLIT><<<grid, block, 0, s>>>(a);
+}
+
 template <typename T, bool C8>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.part_o ? a.runs : a.B), (unsigned)(a.k_heads * a.head_tiles)), block(64 * kWaves);
-    if (a.dim == 64) attn_kernel<T, C8, 64, true><<<grid, block, 0, s>>>(a);
-    else if (a.dim < 64) attn_kernel<T, C8, 64, false><<<grid, block, 0, s>>>(a);
-    else if (a.dim == 128) attn_kernel<T, C8, 128, true><<<grid, block, 0, s>>>(a);
-    else if (a.dim < 128) attn_kernel<T, C8, 128, false><<<grid, block, 0, s>>>(a);
-    else if (a.dim == 256) attn_kernel<T, C8, 256, true><<<grid, block, 0, s>>>(a);
-    else attn_kernel<T, C8, 256, false><<<grid, block, 0, s>>>(a);
+    if (a.part_o) launch_runs<T, C8, true>(a, s);
+    else launch_runs<T, C8, false>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part_o) return e;
     // (64 requests up to 8191, 40 heads: 6.9 us with a workgroup per head, 4.9 flat; 4 requests up to 131072, 64 heads,
