@@ -5,8 +5,9 @@
 // a new token brings only 4 operations per cached value and query head.
 //
 // A workgroup (4 waves) takes one request, one cache head, up to 16 of the query heads that share
-// it, and a range of tokens; each wave takes every fourth step of 32 tokens.  Both products run on
-// 16x16x32 MFMA with the tokens' data straight from global memory in registers, no LDS:
+// it, and a range of tokens; each wave takes every fourth step of 32 tokens (or 16, with halves of the
+// second product).  Both products run on 16x16x32 MFMA with the tokens' data straight from global
+// memory in registers, no LDS:
 //   S^T = K Q^T   A = 16 tokens x 32 entries (16-byte loads of a token's row), B = the heads' q;
 //                 lane (head + 16 g) then holds the scores of its head for tokens 4g .. 4g+3.
 //   O^T = V^T P^T the same lane's weights are already the B operand if slot 8g + j of the product is
@@ -94,6 +95,24 @@ template <bool C8, int N> struct Raw {
     }
 };
 
+// O^T += V^T P^T over the 16 or 32 tokens of a step (NT = 1, 2): operands of two words per 16 tokens.
+template <typename T, int NT>
+__device__ __forceinline__ f32x4 mfma_tokens(const uint32_t* v, const uint32_t* p, f32x4 o) {
+    if constexpr (NT == 2) {
+        return mfma_dense<T>(u32x4{v[0], v[1], v[2], v[3]}, u32x4{p[0], p[1], p[2], p[3]}, o);
+    } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+        const uint2 x = {v[0], v[1]}, y = {p[0], p[1]};
+        if constexpr (T::id == BF16T::id)
+            return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, x), __builtin_bit_cast(s16x4, y), o,
+                                                             0, 0, 0);
+        else
+            return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, x), __builtin_bit_cast(f16x4, y), o, 0,
+                                                         0, 0);
+    }
+}
+
 // Tokens of request b: [start, len), counted from begin = start rounded down to a step of 32.
 struct Span {
     uint32_t start, begin, len;
@@ -170,19 +189,18 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, const Lengths& length
 }
 
 // DP: the head size rounded up to 64, 128 or 256; FULL: it is the head size.  SPLIT: the workgroup takes a run of steps,
-// else request blockIdx.x.
-template <typename T, bool C8, int DP, bool FULL, bool SPLIT>
-__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(AttnArgs a) {
+// else request blockIdx.x.  TOK: tokens of a step, 32 or 16.
+template <typename T, bool C8, int DP, bool FULL, bool SPLIT, int TOK>
+__global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) void attn_kernel(AttnArgs a) {
     constexpr int NK = DP / 32;                 // 32-entry steps of q.k
     constexpr int VEC = DP == 64 ? 4 : 8;       // entries of V a lane holds per token and half
     constexpr int NH = DP == 256 ? 2 : 1;       // 128-entry halves of V
+    constexpr int NT = TOK / 16;                // 16-token halves of a step
+    constexpr int STRIDE = TOK * kWaves;
     constexpr int ES = C8 ? 1 : 2;
     constexpr int W = DP < 128 ? DP : 128;
     __shared__ float lds_o[kWaves][16][W + 4];
     __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
-    // q's operand: in registers, but for heads above 128 entries, where it would not fit beside K, V and O
-    constexpr bool Q_LDS = DP == 256;
-    __shared__ u32x4 lds_q[Q_LDS ? NK : 1][64];
 
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const int wave = uniform(tid >> 6);
@@ -213,11 +231,11 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     const auto page_id = [&](uint32_t t) { return scalar_load(table, min(t >> a.page_shift, last_page)); };
     // a request of its own starts at its first token, unless a window cuts it: its first pages are asked for together
     // with its length
-    int32_t early[4];
+    int32_t early[2 * NT];
     const bool known = !SPLIT && !a.window;
     if (known)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) early[i] = page_id(32 * wave + 16 * (i & 1) + 32 * kWaves * (i >> 1));
+        for (int i = 0; i < 2 * NT; ++i) early[i] = page_id(TOK * wave + 16 * (i % NT) + STRIDE * (i / NT));
     const Span sp = span_of(a, lengths[b]);
     const uint32_t steps = sp.steps(), n_steps = min(steps - run.off, run.left);
     const bool whole_request = n_steps == steps;
@@ -233,23 +251,17 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         run.left = 0;
     }
 
-    u32x4 q[Q_LDS ? 1 : NK];
+    u32x4 q[NK];
     {
         const uint16_t* row = a.Q + b * a.ldq + (int64_t)(head0 + c) * a.dim;
-        const auto load_q = [&](int k) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
             const int d = 32 * k + 8 * g;
-            return c < heads && (FULL || d < a.dim) ? ld16(row + d) : u32x4{0, 0, 0, 0};
-        };
-        if constexpr (Q_LDS) {
-#pragma unroll
-            for (int k = 0; k < NK / kWaves; ++k) lds_q[wave + kWaves * k][lane] = load_q(wave + kWaves * k);
-            __syncthreads();
-        } else {
-#pragma unroll
-            for (int k = 0; k < NK; ++k) q[k] = load_q(k);
+            q[k] = c < heads && (FULL || d < a.dim) ? ld16(row + d) : u32x4{0, 0, 0, 0};
         }
     }
-    // the two 16-token halves of the step at t: the page's id (requested a step ahead), then the byte offset of
+
+    // the 16-token halves of the step at t: the page's id (requested a step ahead), then the byte offset of
     // the half's first token and whether a page holds it
     struct Half {
         int64_t off;
@@ -261,15 +273,15 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         h.off = (h.ok ? id : 0) * page_bytes + (uint64_t)(t & page_mask) * v_step;
         return h;
     };
-    Raw<C8, 8> kr[2][NK];
-    Raw<C8, VEC> vr[NH][8];
+    Raw<C8, 8> kr[NT][NK];
+    Raw<C8, VEC> vr[NH][4 * NT];
     const auto resource = [&](const char* base, int64_t off) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base) + off, (short)0, (int)kBufferEnd,
                                                  0x00020000);
     };
     const auto load_k = [&](const Half* h) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NT; ++j) {
             const auto from = resource(kbase, h[j].off);
 #pragma unroll
             for (int k = 0; k < NK; ++k)
@@ -278,7 +290,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
     };
     const auto load_v = [&](const Half* h) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NT; ++j) {
             const auto from = resource(vbase, h[j].off);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -296,44 +308,43 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         for (int j = 0; j < VEC; ++j) o[n][j] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, ref = 0.0f, l = 0.0f;   // of head c; l: this lane's tokens only
 
-    uint32_t t = first + 32 * wave;
-    Half now[2];
-    int32_t ahead[2];
-    // one step of 32 tokens; MORE: the wave has another step, whose loads are issued on the way.  (The last step is
+    uint32_t t = first + TOK * wave;
+    Half now[NT];
+    int32_t ahead[NT];
+    // one step; MORE: the wave has another step, whose loads are issued on the way.  (The last step is
     // a copy of its own: behind a branch around the loads the compiler would wait for V where K is used.)
     const auto step = [&](auto more) {
         constexpr bool MORE = decltype(more)::value;
-        Half next[2];
-        const uint32_t tn = t + 32 * kWaves;
-        if (MORE) {
-            next[0] = half(tn, ahead[0]);
-            next[1] = half(tn + 16, ahead[1]);
-        }
-        f32x4 s[2];
+        Half next[NT];
+        const uint32_t tn = t + STRIDE;
+        if (MORE)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NT; ++j) next[j] = half(tn + 16 * j, ahead[j]);
+        f32x4 s[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
             s[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
                 const u32x4 x = {kr[j][k].template pair<T>(0), kr[j][k].template pair<T>(1),
                                  kr[j][k].template pair<T>(2), kr[j][k].template pair<T>(3)};
-                s[j] = mfma_dense<T>(x, Q_LDS ? lds_q[k][lane] : q[Q_LDS ? 0 : k], s[j]);
+                s[j] = mfma_dense<T>(x, q[k], s[j]);
             }
         }
         if (MORE) {
             load_k(next);
-            ahead[0] = page_id(tn + 32 * kWaves);
-            ahead[1] = page_id(tn + 32 * kWaves + 16);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) ahead[j] = page_id(tn + STRIDE + 16 * j);
         }
         // outside the span, or in no page: no weight (and no value: 0 * NaN is NaN)
-        const bool whole = t >= sp.start && t + 32 <= last && t + 32 > t && now[0].ok && now[1].ok;
+        const bool whole = t >= sp.start && t + TOK <= last && t + TOK > t && now[0].ok && now[NT - 1].ok;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[j][i] *= s_scale;
         if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t at = t + 16 * j + 4 * g + i;
@@ -344,8 +355,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
                     }
                 }
         }
-        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+        float top = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+        if (NT == 2) top = fmaxf(top, fmaxf(fmaxf(s[NT - 1][0], s[NT - 1][1]), fmaxf(s[NT - 1][2], s[NT - 1][3])));
         if (__any(top > m + 8.0f)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -359,9 +370,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) o[n][j] *= f;
         }
-        u32x4 hi, lo;
+        uint32_t hi[2 * NT], lo[2 * NT];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float p0 = __builtin_amdgcn_exp2f(s[j][2 * i] - ref);
@@ -375,35 +386,35 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : 3) void attn_kernel(At
         for (int n = 0; n < NH; ++n)
 #pragma unroll
             for (int w = 0; w < VEC / 2; ++w) {
-                uint32_t x[8];
+                uint32_t x[4 * NT], even[2 * NT], odd[2 * NT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = vr[n][i].template pair<T>(w);
-                u32x4 even, odd;
+                for (int i = 0; i < 4 * NT; ++i) x[i] = vr[n][i].template pair<T>(w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2 * NT; ++i) {
                     even[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100);
                     odd[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302);
                 }
-                o[n][2 * w] = mfma_dense<T>(even, hi, o[n][2 * w]);
-                o[n][2 * w + 1] = mfma_dense<T>(odd, hi, o[n][2 * w + 1]);
-                o[n][2 * w] = mfma_dense<T>(even, lo, o[n][2 * w]);
-                o[n][2 * w + 1] = mfma_dense<T>(odd, lo, o[n][2 * w + 1]);
+                o[n][2 * w] = mfma_tokens<T, NT>(even, hi, o[n][2 * w]);
+                o[n][2 * w + 1] = mfma_tokens<T, NT>(odd, hi, o[n][2 * w + 1]);
+                o[n][2 * w] = mfma_tokens<T, NT>(even, lo, o[n][2 * w]);
+                o[n][2 * w + 1] = mfma_tokens<T, NT>(odd, lo, o[n][2 * w + 1]);
             }
         if (MORE) {
             load_v(next);
-            now[0] = next[0];
-            now[1] = next[1];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) now[j] = next[j];
             t = tn;
         }
     };
     if (t < last) {
-        now[0] = half(t, known ? early[0] : page_id(t));
-        now[1] = half(t + 16, known ? early[1] : page_id(t + 16));
-        ahead[0] = known ? early[2] : page_id(t + 32 * kWaves);
-        ahead[1] = known ? early[3] : page_id(t + 32 * kWaves + 16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            now[j] = half(t + 16 * j, known ? early[j] : page_id(t + 16 * j));
+            ahead[j] = known ? early[NT + j] : page_id(t + STRIDE + 16 * j);
+        }
         load_k(now);
         load_v(now);
-        while (last - t > 32 * kWaves) step(std::true_type());
+        while (last - t > STRIDE) step(std::true_type());
         step(std::false_type());
     }
 
@@ -590,15 +601,21 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
     write_joined<T>(a, b, h, d, sum, l, top);
 }
 
+// Tokens of a step.  16 leave room for more waves, or for heads above 128 entries without spills (16 requests up to
+// 8192, 16/4 heads of 256: 57.7 us against 71.1; 32/8 heads of 64: 34.5 against 35.9; 64 up to 8191 on an 8-bit cache:
+// 102.5 against 104.3); 32 keep more of a long 16-bit cache of 128-entry heads in flight per wave (4 requests up to
+// 131072: 236.8 against 241.7, 32 up to 4096: 58.4 against 59.8), and halve the steps of a request that is not cut.
+template <bool C8, int DP, bool FULL, bool SPLIT>
+constexpr int kTok = DP == 256 || (SPLIT && !(DP == 128 && FULL && !C8)) ? 16 : 32;
 template <typename T, bool C8, bool SPLIT>
 void launch_runs(const AttnArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(SPLIT ? a.runs : a.B), (unsigned)(a.k_heads * a.head_tiles)), block(64 * kWaves);
-    if (a.dim == 64) attn_kernel<T, C8, 64, true, SPLIT><<<grid, block, 0, s>>>(a);
-    else if (a.dim < 64) attn_kernel<T, C8, 64, false, SPLIT><<<grid, block, 0, s>>>(a);
-    else if (a.dim == 128) attn_kernel<T, C8, 128, true, SPLIT><<<grid, block, 0, s>>>(a);
-    else if (a.dim < 128) attn_kernel<T, C8, 128, false, SPLIT><<<grid, block, 0, s>>>(a);
-    else if (a.dim == 256) attn_kernel<T, C8, 256, true, SPLIT><<<grid, block, 0, s>>>(a);
-    else attn_kernel<T, C8, 256, false, SPLIT><<<grid, block, 0, s>>>(a);
+    if (a.dim == 64) attn_kernel<T, C8, 64, true, SPLIT, kTok<C8, 64, true, SPLIT>><<<grid, block, 0, s>>>(a);
+    else if (a.dim < 64) attn_kernel<T, C8, 64, false, SPLIT, kTok<C8, 64, false, SPLIT>><<<grid, block, 0, s>>>(a);
+    else if (a.dim == 128) attn_kernel<T, C8, 128, true, SPLIT, kTok<C8, 128, true, SPLIT>><<<grid, block, 0, s>>>(a);
+    else if (a.dim < 128) attn_kernel<T, C8, 128, false, SPLIT, kTok<C8, 128, false, SPLIT>><<<grid, block, 0, s>>>(a);
+    else if (a.dim == 256) attn_kernel<T, C8, 256, true, SPLIT, kTok<C8, 256, true, SPLIT>><<<grid, block, 0, s>>>(a);
+    else attn_kernel<T, C8, 256, false, SPLIT, kTok<C8, 256, false, SPLIT>><<<grid, block, 0, s>>>(a);
 }
 
 template <typename T, bool C8>

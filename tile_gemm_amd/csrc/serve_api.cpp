@@ -113,7 +113,7 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     const uint64_t most = window ? std::min<uint64_t>(p.cap, (uint64_t)p.window + 31) : p.cap;
     const uint64_t steps = (uint64_t)B * ((most + 31) / 32);
     // 256 CUs hold three workgroups each; of those for heads above 128 entries two, but one streams as fast and leaves
-    // fewer parts (16 requests up to 8192, 16/4 heads of 256: 75 us with 256 runs, 88 with 768).  Where a page holds
+    // fewer parts (16 requests up to 8192, 16/4 heads of 256: 57.7 us with 256 runs, 59.4 with 512).  Where a page holds
     // a head's tokens one after another, two a CU are as fast or faster for the same reason (256 requests up to
     // 2048, 32/8 heads, pages of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209).
     const int64_t runs = kv->dim > 128 ? 256 : kv->head_stride > kv->token_stride ? 512 : 768;
