@@ -112,11 +112,16 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     const int64_t rows = (int64_t)kv->heads * p.head_tiles;
     const uint64_t most = window ? std::min<uint64_t>(p.cap, (uint64_t)p.window + 31) : p.cap;
     const uint64_t steps = (uint64_t)B * ((most + 31) / 32);
-    // 256 CUs hold three workgroups each; of those for heads above 128 entries two, but one streams as fast and leaves
-    // fewer parts (16 requests up to 8192, 16/4 heads of 256: 57.7 us with 256 runs, 59.4 with 512).  Where a page holds
-    // a head's tokens one after another, two a CU are as fast or faster for the same reason (256 requests up to
-    // 2048, 32/8 heads, pages of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209).
-    const int64_t runs = kv->dim > 128 ? 256 : kv->head_stride > kv->token_stride ? 512 : 768;
+    // 256 CUs hold three or four workgroups each, two of those for heads above 128 entries.  Four pay for smaller heads
+    // of 16 bits (16 requests up to 4096, 16/4 heads of 96: 17.0 us with 1024 runs, 18.3 with 768; 64 requests up to 8191
+    // on an 8-bit cache: 113.9 and 112.4).  Fewer stream as fast where each has long stretches to itself, and leave
+    // fewer parts: one a CU for heads above 128 (16 requests up to 8192, 16/4 heads of 256: 57.7 us with 256 runs, 59.4
+    // with 512), two where a page holds a head's tokens one after another (256 requests up to 2048, 32/8 heads, pages
+    // of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209).
+    const int64_t runs = kv->dim > 128                        ? 256
+                         : kv->head_stride > kv->token_stride ? 512
+                         : kv->dim < 128 && kv->dtype != HTS_FP8_E4M3 ? 1024
+                                                                      : 768;
     p.target = (int32_t)std::max<int64_t>(1, runs / rows);
     const uint64_t least = std::min<uint64_t>(std::max<uint64_t>(3 * steps / p.target, 8), 16);   // as in the kernel
     p.runs = (int32_t)std::min<uint64_t>(p.target, std::max<uint64_t>(B, (steps + least - 1) / least));
