@@ -64,7 +64,7 @@ hipError_t launch_attn(const AttnArgs& a, hipStream_t) {
         if (steps >= (uint64_t(1) << 31) || a.B > kMaxSplitRequests) complain("too many steps to split");
         for (uint64_t total : {steps, steps / 2 + 1, (uint64_t)a.B, (uint64_t)1}) {
             const uint64_t even = (total + a.runs - 1) / a.runs;
-            const uint64_t few = std::min<uint64_t>(std::max<uint64_t>((uint32_t)(3 * total) / a.target, 8), 16);
+            const uint64_t few = std::min<uint64_t>(std::max<uint64_t>((uint32_t)(3 * total) / a.target, 4), 16);
             const uint64_t per = std::max(even, std::min<uint64_t>(few, (total + a.B - 1) / a.B));
             if ((total + per - 1) / per > (uint64_t)a.runs) complain("more runs than workgroups");
         }

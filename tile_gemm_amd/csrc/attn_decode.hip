@@ -95,6 +95,13 @@ template <bool C8, int N> struct Raw {
     }
 };
 
+// Two floats to two 16-bit values in a word by one conversion: to nearest for bfloat16, towards zero for binary16.
+// What it leaves out goes to the second part, whose own rounding is below 2^-16 of the value either way.
+template <typename T> __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
+    if constexpr (T::id == BF16T::id) return narrow2<T>(lo, hi);
+    else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+}
+
 // O^T += V^T P^T over the 16 or 32 tokens of a step (NT = 1, 2): operands of two words per 16 tokens.
 template <typename T, int NT>
 __device__ __forceinline__ f32x4 mfma_tokens(const uint32_t* v, const uint32_t* p, f32x4 o) {
@@ -167,10 +174,10 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, const Lengths& length
     const uint32_t in = wave_scan(mine), total = __builtin_amdgcn_readlane(in, 63);
     Run r;
     // An even share, but where that is short a longer run, down to a third as many of them: each costs a start, an
-    // end and its parts (one request of 4096 tokens, 32 heads: 19.8 us with runs of 6 steps, 18.4 with 16; 8
-    // requests up to 1024, 32/8 heads: 13.9 with 8, 16.1 with 16) -- and not longer for that than the requests are, which
-    // cost as much each.
-    const uint32_t few = min(min(max(3 * total / a.target, 8u), 16u), (total + a.B - 1) / a.B);
+    // end and its parts (one request of 4096 tokens, 32 heads: 19.8 us with runs of 6 steps, 18.4 with 16; 16 of up to
+    // 300 in a table for 8192, 32/8 heads: 13.0 with 4, 14.8 with 8) -- and not longer for that than the requests are,
+    // which cost as much each.
+    const uint32_t few = min(min(max(3 * total / a.target, 4u), 16u), (total + a.B - 1) / a.B);
     r.per = max((total + gridDim.x - 1) / gridDim.x, few);
     const uint32_t pos = x * r.per;
     r.left = pos < total ? min(r.per, total - pos) : 0;
@@ -378,9 +385,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
                 const float p0 = __builtin_amdgcn_exp2f(s[j][2 * i] - ref);
                 const float p1 = __builtin_amdgcn_exp2f(s[j][2 * i + 1] - ref);
                 l += p0 + p1;
-                const uint32_t h0 = narrow<T>(p0), h1 = narrow<T>(p1);
-                hi[2 * j + i] = h0 | (h1 << 16);
-                lo[2 * j + i] = narrow<T>(p0 - widen<T>(h0)) | (narrow<T>(p1 - widen<T>(h1)) << 16);
+                const uint32_t h = upper2<T>(p0, p1);
+                hi[2 * j + i] = h;
+                lo[2 * j + i] = upper2<T>(p0 - widen<T>(h & 0xFFFFu), p1 - widen<T>(h >> 16));
             }
 #pragma unroll
         for (int n = 0; n < NH; ++n)
@@ -457,8 +464,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
             } else {
                 const float inv = den == 0.0f ? 0.0f : v_scale / den;
                 uint16_t* out = a.O + b * a.ldo + (int64_t)(head0 + h) * a.dim + at;
-                *reinterpret_cast<uint2*>(out) = uint2{narrow<T>(sum[0] * inv) | (narrow<T>(sum[1] * inv) << 16),
-                                                       narrow<T>(sum[2] * inv) | (narrow<T>(sum[3] * inv) << 16)};
+                *reinterpret_cast<uint2*>(out) = uint2{narrow2<T>(sum[0] * inv, sum[1] * inv),
+                                                       narrow2<T>(sum[2] * inv, sum[3] * inv)};
                 if (at == 0 && a.lse)
                     a.lse[(int64_t)b * a.q_heads + head0 + h] = den == 0.0f ? -INFINITY : (top - kShift + log2f(den)) * kLn2;
             }
@@ -488,8 +495,7 @@ template <typename T>
 __device__ __forceinline__ void write_joined(const AttnArgs& a, int b, int h, int d, f32x4 sum, float l, float top) {
     const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h / (a.q_heads / a.k_heads)] : 1.0f) / l;
     *reinterpret_cast<uint2*>(a.O + b * a.ldo + (int64_t)h * a.dim + d) =
-        uint2{narrow<T>(sum[0] * inv) | (narrow<T>(sum[1] * inv) << 16),
-              narrow<T>(sum[2] * inv) | (narrow<T>(sum[3] * inv) << 16)};
+        uint2{narrow2<T>(sum[0] * inv, sum[1] * inv), narrow2<T>(sum[2] * inv, sum[3] * inv)};
     if (d == 0 && a.lse) a.lse[(int64_t)b * a.q_heads + h] = l == 0.0f ? -INFINITY : (top - kShift + log2f(l)) * kLn2;
 }
 

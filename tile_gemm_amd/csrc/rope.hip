@@ -31,8 +31,7 @@ template <typename T, int V> __device__ __forceinline__ void store_v(uint16_t* p
     if (V == 8) {
         stream16(p, narrow8<T>(f));
     } else {
-        *reinterpret_cast<uint2*>(p) = uint2{narrow<T>(f[0]) | (narrow<T>(f[1]) << 16),
-                                             narrow<T>(f[2]) | (narrow<T>(f[3]) << 16)};
+        *reinterpret_cast<uint2*>(p) = uint2{narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3])};
     }
 }
 template <int V> __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* f, float scale) {

@@ -123,7 +123,7 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
                          : kv->dim < 128 && kv->dtype != HTS_FP8_E4M3 ? 1024
                                                                       : 768;
     p.target = (int32_t)std::max<int64_t>(1, runs / rows);
-    const uint64_t least = std::min<uint64_t>(std::max<uint64_t>(3 * steps / p.target, 8), 16);   // as in the kernel
+    const uint64_t least = std::min<uint64_t>(std::max<uint64_t>(3 * steps / p.target, 4), 16);   // as in the kernel
     p.runs = (int32_t)std::min<uint64_t>(p.target, std::max<uint64_t>(B, (steps + least - 1) / least));
     p.split = B >= 1 && B <= hts::kMaxSplitRequests && most > hts::kAttnWholeTokens && steps < (uint64_t)kInt32;
     if (p.split) {

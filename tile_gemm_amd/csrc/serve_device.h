@@ -17,10 +17,18 @@ template <typename T> __device__ __forceinline__ void widen8(u32x4 v, float* f) 
     }
 }
 
+// Two floats to two 16-bit values in a word, round to nearest even (one packed conversion for bfloat16).
+template <typename T> __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    if constexpr (T::id == BF16T::id) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+    else return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+}
+
 template <typename T> __device__ __forceinline__ u32x4 narrow8(const float* f) {
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = narrow<T>(f[2 * i]) | (narrow<T>(f[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) v[i] = narrow2<T>(f[2 * i], f[2 * i + 1]);
     return v;
 }
 
