@@ -723,3 +723,35 @@ def test_debug_mode_refuses_short_buffers(monkeypatch):
         assert b"k_cache needs" in L.hts_last_error()
     finally:
         short.free()
+
+
+def test_two_attention_calls_at_once():
+    # split calls on two streams, each with a workspace of its own, many times over
+    a = _attn_case(128, 16, 2, 16, "token", "same", [9000, 70, 0], "bf16", 41)
+    b = _attn_case(128, 8, 8, 64, "head", "fp8", [3000, 1, 777, 5000], "bf16", 42)
+    calls = [(q, c, i32(t)[:, :w].contiguous(), i32(n)) for (q, c, t, w), n in ((a, [9000, 70, 0]), (b, [3000, 1, 777, 5000]))]
+    want = [hts.paged_attn(*x) for x in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for k in (0, 1):
+            got[k].append(hts.paged_attn(*calls[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(x, want[k]) for x in got[k])
+
+
+def test_one_page_for_all_and_for_a_whole_row():
+    # the same page many times in a row of the table, and the same row for every request
+    c = hts.kv_cache(2, 16, 2, 64, torch.float16, DEV)
+    g = np.random.default_rng(3)
+    c.k.copy_(normal(g, c.k.shape, "f16"))
+    c.v.copy_(normal(g, c.v.shape, "f16"))
+    q = normal(g, (1, 4 * 64), "f16").expand(3, -1).contiguous()
+    table = np.full((3, 80), 1)
+    lengths = [1280, 16, 1279]
+    out = hts.paged_attn(q, c, i32(table), i32(lengths))
+    _check_attn(q, c, table, 80, lengths, 4, 0, 64 ** -0.5, out, None, "f16")
+    # 1280 tokens that repeat 16 tokens 80 times: the attention over the 16
+    assert float((out[0].float() - out[1].float()).abs().max()) <= 2.0 ** -10 * float(c.v.float().abs().max())
