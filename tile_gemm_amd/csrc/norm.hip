@@ -8,38 +8,50 @@
 // Bound by HBM: block, R and a per-token gate in, R' and Y out, once each.  The outputs are written past the
 // caches' normal lines (non-temporal): another XCD will read them, and the inputs keep their place (1000 x
 // 16384: 24.4 us against 32 with ordinary stores).  16384 x 4096, layer norms on both sides and a sigmoid gate:
-// 138 us, 4.9 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.8 us.
+// 131-139 us, 4.8-5.1 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.6 us.  Sums go by row moves within a wave and one
+// barrier each (10 x 6568, two layer norms: 6.1 us against 7.5 with shuffles through LDS and two barriers).
 #include "serve_device.h"
 #include "serve_internal.h"
 
 namespace hts {
 namespace {
 
-// Sum over the threads of a row: LANES of a wave, or (LANES = 0) the whole workgroup.
+template <int CTRL, int ROWS> __device__ __forceinline__ float add_moved(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xF, false));
+}
+// Sum over each row of 16 lanes, in every lane of it (row rotations by 8, 4, 2 and 1: no trip through LDS).
+__device__ __forceinline__ float sum16(float x) {
+    return add_moved<0x121, 0xF>(add_moved<0x122, 0xF>(add_moved<0x124, 0xF>(add_moved<0x128, 0xF>(x))));
+}
+
+// Sum over the threads of a row: LANES of a wave, or (LANES = 0) the whole workgroup, with one barrier: lds is used
+// by one sum only.
 template <int LANES> __device__ __forceinline__ float row_sum(float v, float* lds) {
-#pragma unroll
-    for (int o = (LANES ? LANES : 64) / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    if (LANES) return v;
-    const int waves = blockDim.x >> 6;
-    if (waves == 1) return v;
-    __syncthreads();                     // the last sum has been read by all
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.0f;
-    for (int w = 0; w < waves; ++w) s += lds[w];
-    return s;
+    v = sum16(v);
+    if (LANES == 16) return v;
+    if (LANES == 32) return v + __shfl_xor(v, 16);
+    v = add_moved<0x142, 0xA>(v);        // row 0's sum to row 1, row 2's to row 3
+    v = add_moved<0x143, 0xC>(v);        // row 1's to rows 2 and 3: lane 63 has all
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+    if (waves > 1) {
+        if (lane == 63) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        const float part = lds[lane & 15];
+        v = sum16((lane & 15) < waves ? part : 0.0f);
+    }
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 template <typename T, bool R32, int LANES, int CH>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormArgs a) {
-    __shared__ float lds[16];
+    __shared__ float sums[4][16];        // a layer norm takes two sums, and there are two norms
     const int per_row = LANES ? LANES : blockDim.x, me = LANES ? threadIdx.x % LANES : threadIdx.x;
     const int64_t m = LANES ? (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES : blockIdx.x;
     if (LANES && m >= a.M) return;       // rows of one wave end apart: their shuffles stay within a row
     float x[CH][8];
     // entry of chunk c; past the row's end a chunk holds zeros and stays out of the sums
     const auto col = [&](int c) { return (c * per_row + me) * 8; };
-    const auto norm = [&](int kind, float eps, const uint16_t* w, const uint16_t* b) {
+    const auto norm = [&](int kind, float eps, const uint16_t* w, const uint16_t* b, float (*lds)[16]) {
         const float inv_n = 1.0f / (float)a.N;
         // the weights' loads go out ahead of the sums
         u32x4 wv[CH], bv[CH];
@@ -54,7 +66,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormA
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += x[c][e];
-            const float mean = row_sum<LANES>(s, lds) * inv_n;
+            const float mean = row_sum<LANES>(s, lds[0]) * inv_n;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
                 if (col(c) < a.N)
@@ -66,7 +78,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormA
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e) q = fmaf(x[c][e], x[c][e], q);
-        const float r = 1.0f / sqrtf(row_sum<LANES>(q, lds) * inv_n + eps);
+        const float r = 1.0f / sqrtf(row_sum<LANES>(q, lds[1]) * inv_n + eps);
 #pragma unroll
         for (int c = 0; c < CH; ++c)
             if (col(c) < a.N) {
@@ -101,7 +113,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormA
             if (R32) rv[c][R32 ? 1 : 0] = ld16(p + 16);
         }
     }
-    if (a.post != HTS_NORM_NONE) norm(a.post, a.post_eps, a.post_w, a.post_b);
+    if (a.post != HTS_NORM_NONE) norm(a.post, a.post_eps, a.post_w, a.post_b, sums);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         if (col(c) >= a.N) continue;
@@ -145,7 +157,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormA
         }
     }
     if (!a.Y) return;
-    if (a.pre != HTS_NORM_NONE) norm(a.pre, a.pre_eps, a.pre_w, a.pre_b);
+    if (a.pre != HTS_NORM_NONE) norm(a.pre, a.pre_eps, a.pre_w, a.pre_b, sums + 2);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
         if (col(c) < a.N) stream16(a.Y + m * a.ldy + col(c), narrow8<T>(x[c]));
