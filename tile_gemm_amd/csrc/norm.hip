@@ -8,7 +8,7 @@
 // Bound by HBM: block, R and a per-token gate in, R' and Y out, once each.  The outputs are written past the
 // caches' normal lines (non-temporal): another XCD will read them, and the inputs keep their place (1000 x
 // 16384: 24.4 us against 32 with ordinary stores).  16384 x 4096, layer norms on both sides and a sigmoid gate:
-// 131-139 us, 4.8-5.1 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.6 us.  Sums go by row moves within a wave and one
+// 126-135 us, 5.0-5.3 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.6 us.  Sums go by row moves within a wave and one
 // barrier each (10 x 6568, two layer norms: 6.1 us against 7.5 with shuffles through LDS and two barriers).
 #include "serve_device.h"
 #include "serve_internal.h"
