@@ -391,8 +391,10 @@ hts_status hts_rope_cache(const hts_rope_desc* d, const double* turns, int64_t T
  * all), whose block-table entry names a page of the cache (other tokens are left out):
  *     s_t = scale * q . k_t,  O = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m),  m = max_t s_t
  * with K and V multiplied by their head's scale for an 8-bit cache.  Scores, maximum, sums and
- * accumulators are 32-bit; O is rounded once to dtype.  A request with no token (or only scores of
- * minus infinity) gets zeros.  lse (float [B, q_heads], or NULL) receives m + ln sum e^(s_t - m),
+ * accumulators are 32-bit.  Weights are held to 2^-24 of their value for HTS_BF16, and for HTS_F16 to
+ * 2^-21, or 2^-43 of the largest weight where that is more.  O is rounded once to dtype.  A request
+ * with no token (or only scores of minus infinity) gets zeros.  An infinity in the V of a token that
+ * counts gives NaN or infinity in its entry.  lse (float [B, q_heads], or NULL) receives m + ln sum e^(s_t - m),
  * minus infinity for such a request: two calls over parts of a context can be joined by it.
  * What the cache holds past a request's tokens is never used (NaN there does no harm).
  * Q, O: [B, q_heads*dim] in dtype (HTS_F16 / HTS_BF16), 16-byte aligned, leading dimensions

@@ -446,6 +446,72 @@ def test_paged_attn_small_weights_add_up(dtype):
         c.v[first // page, first % page] = 1.0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_paged_attn_small_weights_beside_a_large_one(dtype, dim):
+    # one wave forms large and small weights together: the call is not split (no room for its parts), and every wave
+    # starts with a token of weight 1 and value 0; 100000 others have weights e^-9 to e^-20.25 and the value 100
+    page, n, heavy, v = 64, 100008, 8, 100.0
+    pages = -(-n // page)
+    c = hts.kv_cache(pages, page, 1, dim, TORCH[dtype], DEV)
+    c.k[..., 0] = -18.0
+    c.v.fill_(v)
+    c.k[0, 0:16 * heavy:16, 0, 0] = 0.0          # waves start at tokens 0, 16, 32, 48 or 0, 32, 64, 96
+    c.k[1, 0:16 * heavy - 64:16, 0, 0] = 0.0
+    c.v[0, 0:64:16] = 0.0
+    c.v[1, 0:64:16] = 0.0
+    by = [0.5, 1.0, 1.0625, 1.125]               # scores of -9, -18, -19.125, -20.25: exact in either type
+    q = torch.zeros((1, len(by) * dim), dtype=TORCH[dtype], device=DEV)
+    for h, x in enumerate(by):
+        q[0, h * dim] = x
+    lse = torch.empty((1, len(by)), device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    out = hts.paged_attn(q, c, table, i32([n]), scale=1.0, lse=lse, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    got = f64(out)[0].reshape(len(by), dim)
+    for h, x in enumerate(by):
+        w = np.exp(-18.0 * x)
+        small = (n - heavy) * w
+        want = small * v / (heavy + small)
+        # half a step of the type; a weight's own 2^-21, or 2^-43 of the largest weight; the exponential's argument
+        # (|s| log2 e below 32: 2^-20 of its rounding) and its last place; sums of a lane's pairs (16 lanes share the
+        # tokens) and of a wave's steps of 16 tokens, in 32 bits
+        tol = ref.EPS[dtype] / 2 + 2.0 ** -21 + 2.0 ** -43 / w + 2.0 ** -19 + (n / 32 + n / 64) * 2.0 ** -24
+        assert np.all(np.abs(got[h] - want) <= tol * want), (dim, x, got[h][:2], want, tol)
+        assert abs(float(lse[0, h]) - np.log(heavy + small)) <= 2.0 ** -18 + n / 32 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("cache", ["same", "fp8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 192])
+def test_paged_attn_values_that_cancel(dtype, dim, cache):
+    # two tokens whose weighted values nearly cancel: what is left shows the weights' own precision.  A head's weights
+    # are 1 and about a / b, its values -a and b.
+    page = 16
+    ratio = [(8, 15, -1), (8, 15, -3), (8, 13, 1), (8, 15, 1), (9, 14, 3), (9, 11, -3), (11, 13, -1), (9, 13, 3)]
+    hk = len(ratio)
+    ct = TORCH[dtype] if cache == "same" else TORCH["fp8"]
+    k, v = torch.zeros((1, page, hk, dim)), torch.zeros((1, page, hk, dim))
+    for h, (a, b, off) in enumerate(ratio):
+        left = np.log(a / b * (1 + off * 2.0 ** -13))   # the second token's score, in as many entries as it takes
+        for d in range(8):
+            part = torch.tensor(left, dtype=torch.float32).to(ct).float()
+            k[0, 1, h, d] = part
+            left -= float(part)
+        v[0, 0, h], v[0, 1, h] = -a, b
+    c = hts.KVCache(k.to(ct).to(DEV), v.to(ct).to(DEV))
+    q = torch.ones((1, hk * dim), dtype=TORCH[dtype], device=DEV)
+    got = f64(hts.paged_attn(q, c, i32([[0]]), i32([2]), scale=1.0))[0].reshape(hk, dim)
+    kk, vv = f64(c.k)[0], f64(c.v)[0]
+    for h in range(hk):
+        p = np.exp(np.array([0.0, kk[1, h].sum()]))
+        want = p @ vv[:2, h] / p.sum()
+        # half a step of the type, and relative to the second value's weight: the weight's 2^-21; its argument, up to
+        # 8 (2^-22 ln 2); the exponential's last place (2^-23); a score below 1 summed from 8 terms that shrink by 2^-4
+        # and more, and scaled (2^-23); two sums (2^-23 together)
+        tol = ref.EPS[dtype] / 2 * np.abs(want) + (2.0 ** -21 + 0.7 * 2.0 ** -22 + 3 * 2.0 ** -23) * p[1] * vv[1, h] / p.sum()
+        assert np.all(np.abs(got[h] - want) <= tol), (h, got[h][:2], want[:2], tol[:2])
+
+
 @pytest.mark.parametrize("lengths", [[100, 3], [9000, 70, 0]])
 def test_paged_attn_in_a_graph(lengths):
     # captured once at one set of lengths, replayed at others with eager work in between

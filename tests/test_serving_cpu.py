@@ -249,3 +249,30 @@ def test_attention_kernels_respect_wait_states(tmp_path):
         return op == op2 and not (regs(x) | regs(y)) & r and (regs(acc) == r or not regs(acc) & r)
     bad = [x for x in violations(text, required_waits(flags, hipcc)) if not (x[2].startswith("v_mfma") and in_order(x[1], x[2]))]
     assert not bad, f"{len(bad)} early reads, first: {bad[:3]}"
+
+
+def test_shorter_products_respect_wait_states(tmp_path, monkeypatch):
+    # the products over 16 tokens, as producers, and any accumulator that passes between products of two kinds
+    import os
+    import isa_waitstates as iw
+    from tile_gemm_amd import build as hb
+    try:
+        hipcc = hb.hipcc()
+    except RuntimeError:
+        pytest.skip("hipcc not available")
+    monkeypatch.setattr(iw, "_PROBE_HEAD", iw._PROBE_HEAD + "typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));\n")
+    monkeypatch.setattr(iw, "PROBE_OPS", {
+        "v_mfma_f32_16x16x16_f16": "const f16x4* q = (const f16x4*)H8; "
+                                   "acc = __builtin_amdgcn_mfma_f32_16x16x16f16(q[l], q[l + 64], acc, 0, 0, 0);"})
+    flags = [f for f in hb.COMMON if f != "-fPIC"] + hb.VGPR_FORM
+    text = iw.device_asm(os.path.join(hb.CSRC, "attn_decode.hip"), str(tmp_path / "k.s"), flags, hipcc)
+    need = iw.required_waits(flags, hipcc)
+    assert need["v_mfma_f32_16x16x16_f16"] > 1 and "v_mfma_f32_16x16x16_f16" in text
+    # of one kind results land in the order of issue: a product may write registers that an earlier one wrote
+    late = [x for x in iw.violations(text, need) if x[2].split()[0] != x[1].split()[0]]
+    assert not late, late[:3]
+    same = [x for x in iw.violations(text, need) if x[2].split()[0] == x[1].split()[0]]
+    for _, first, second in same:
+        out = iw._regs(iw._ops(first)[1][0])
+        _, a, b, acc = iw._ops(second)[1][:4]
+        assert not out & (iw._regs(a) | iw._regs(b)) and (iw._regs(acc) == out or not iw._regs(acc) & out), (first, second)

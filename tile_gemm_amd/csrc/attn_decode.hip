@@ -17,8 +17,9 @@
 // So the maximum, the sum and the accumulators of a head stay in the lanes of that head, and no
 // value crosses lanes in the loop but the maximum -- and that only when a score passes the last
 // reference by 2^8, which rescales; below that the weights stay in range and nothing is lost.
-// Weights are split into two 16-bit parts (their sum holds 16 bits and more), so that the product
-// with V rounds them no further than 2^-16: the matrix cores are idle most of the time.
+// Weights go to the product with V in 16-bit parts that hold 24 bits (bfloat16, three parts) or 22 (binary16, two, the
+// second 2^11 times as large, so that it reaches below binary16's smallest value): the matrix cores are idle most of the
+// time (no case measured is slower than with two unscaled parts).
 // K's registers are reloaded for the next step as soon as the scores are out, V's as soon as O is.
 //
 // The work is divided evenly: per cache head, the steps of all requests in a row are cut into as
@@ -37,8 +38,7 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-// Weights are 2^(s - m + 7): at most 2^15, since m is at least the maximum less 8, which binary16 holds, and still
-// above its smallest value, 2^-24, where they are 2^-31 of the largest (many such weights add up in a long context).
+// Weights are 2^(s - m + 7): at most 2^15, since m is at least the maximum less 8, which binary16 holds.
 constexpr float kShift = 7.0f;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -95,28 +95,57 @@ template <bool C8, int N> struct Raw {
     }
 };
 
-// Two floats to two 16-bit values in a word by one conversion: to nearest for bfloat16, towards zero for binary16.
-// What it leaves out goes to the second part, whose own rounding is below 2^-16 of the value either way.
-template <typename T> __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
-    if constexpr (T::id == BF16T::id) return narrow2<T>(lo, hi);
-    else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+// Two weights as 16-bit parts, a word each.  A part takes what those before it left out, which 32 bits hold exactly.
+//   bfloat16: three parts of 8 bits, to nearest: 24 bits, a 32-bit weight's own.
+//   binary16: 11 bits, towards zero, then 2^11 times the rest, to nearest: off by at most 2^-21 of the weight, or 2^-36
+//             where that is more (below 2^-14 the first part's steps are 2^-24).  The largest weight is 2^7 and more, so
+//             a token of a long context loses at most 2^-43 of the largest, however many there are of them; with the
+//             rest unscaled it lost up to 2^-31, always downwards (100000 tokens of e^-18 beside a large one: 2%).
+constexpr float kRest = 2048.0f;
+template <typename T> constexpr int kParts = T::id == BF16T::id ? 3 : 2;
+template <typename T> __device__ __forceinline__ void split2(float lo, float hi, uint32_t* part) {
+    if constexpr (T::id == BF16T::id) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            part[k] = narrow2<T>(lo, hi);
+            lo -= widen<T>(part[k] & 0xFFFFu);
+            hi -= widen<T>(part[k] >> 16);
+        }
+    } else {
+        part[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+        part[1] = narrow2<T>((lo - widen<T>(part[0] & 0xFFFFu)) * kRest, (hi - widen<T>(part[0] >> 16)) * kRest);
+    }
 }
 
-// O^T += V^T P^T over the 16 or 32 tokens of a step (NT = 1, 2): operands of two words per 16 tokens.
+// O^T += V^T P^T over the 16 (binary16 only) or 32 tokens of a step (NT = 1, 2): operands of two words per 16 tokens.
 template <typename T, int NT>
 __device__ __forceinline__ f32x4 mfma_tokens(const uint32_t* v, const uint32_t* p, f32x4 o) {
     if constexpr (NT == 2) {
         return mfma_dense<T>(u32x4{v[0], v[1], v[2], v[3]}, u32x4{p[0], p[1], p[2], p[3]}, o);
     } else {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-        const uint2 x = {v[0], v[1]}, y = {p[0], p[1]};
-        if constexpr (T::id == BF16T::id)
-            return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, x), __builtin_bit_cast(s16x4, y), o,
-                                                             0, 0, 0);
-        else
-            return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, x), __builtin_bit_cast(f16x4, y), o, 0,
-                                                         0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, uint2{v[0], v[1]}),
+                                                     __builtin_bit_cast(f16x4, uint2{p[0], p[1]}), o, 0, 0, 0);
+    }
+}
+
+// The same with the weights in their parts.  Of bfloat16's three on 16 tokens the first two share a product of 32 places,
+// and the third takes such a one too: an accumulator that goes from the longer product straight into the shorter one is
+// read before it is whole (the compiler leaves no wait there).
+template <typename T, int NT>
+__device__ __forceinline__ f32x4 mfma_weights(const uint32_t* v, const uint32_t (*p)[2 * NT], f32x4 o) {
+    if constexpr (T::id == F16T::id) {
+        const f32x4 rest = mfma_tokens<T, NT>(v, p[1], f32x4{0, 0, 0, 0});
+        o = mfma_tokens<T, NT>(v, p[0], o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(rest[i], 1.0f / kRest, o[i]);
+        return o;
+    } else if constexpr (NT == 2) {
+        return mfma_tokens<T, NT>(v, p[2], mfma_tokens<T, NT>(v, p[1], mfma_tokens<T, NT>(v, p[0], o)));
+    } else {
+        const u32x4 twice = {v[0], v[1], v[0], v[1]};
+        return mfma_dense<T>(twice, u32x4{p[2][0], p[2][1], 0, 0},
+                             mfma_dense<T>(twice, u32x4{p[0][0], p[0][1], p[1][0], p[1][1]}, o));
     }
 }
 
@@ -377,7 +406,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) o[n][j] *= f;
         }
-        uint32_t hi[2 * NT], lo[2 * NT];
+        uint32_t p[kParts<T>][2 * NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -385,9 +414,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
                 const float p0 = __builtin_amdgcn_exp2f(s[j][2 * i] - ref);
                 const float p1 = __builtin_amdgcn_exp2f(s[j][2 * i + 1] - ref);
                 l += p0 + p1;
-                const uint32_t h = upper2<T>(p0, p1);
-                hi[2 * j + i] = h;
-                lo[2 * j + i] = upper2<T>(p0 - widen<T>(h & 0xFFFFu), p1 - widen<T>(h >> 16));
+                uint32_t part[kParts<T>];
+                split2<T>(p0, p1, part);
+#pragma unroll
+                for (int k = 0; k < kParts<T>; ++k) p[k][2 * j + i] = part[k];
             }
 #pragma unroll
         for (int n = 0; n < NH; ++n)
@@ -401,10 +431,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
                     even[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100);
                     odd[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302);
                 }
-                o[n][2 * w] = mfma_tokens<T, NT>(even, hi, o[n][2 * w]);
-                o[n][2 * w + 1] = mfma_tokens<T, NT>(odd, hi, o[n][2 * w + 1]);
-                o[n][2 * w] = mfma_tokens<T, NT>(even, lo, o[n][2 * w]);
-                o[n][2 * w + 1] = mfma_tokens<T, NT>(odd, lo, o[n][2 * w + 1]);
+                o[n][2 * w] = mfma_weights<T, NT>(even, p, o[n][2 * w]);
+                o[n][2 * w + 1] = mfma_weights<T, NT>(odd, p, o[n][2 * w + 1]);
             }
         if (MORE) {
             load_v(next);
@@ -426,26 +454,30 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 ? 2 : TOK == 16 ? 4 : 3) voi
     }
 
     // the four waves' parts of each head, weighted by their maxima and summed in order
+    // (its places are worked out here: kept through the loop they would take registers that it does not have)
+    int late = tid;
+    asm volatile("" : "+v"(late));
+    const int lc = late & 15, lg = (late & 63) >> 4;
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    if (g == 0) {
-        lds_m[wave][c] = m;
-        lds_l[wave][c] = l;
+    if (lg == 0) {
+        lds_m[wave][lc] = m;
+        lds_l[wave][lc] = l;
     }
     const int64_t part = ((int64_t)slot * gridDim.y + y) * a.tile_heads;
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
         if (n) __syncthreads();
         // lane (c, g) holds 4 VEC entries of head c in a row, from 4 VEC g on in its half
-        if (c < heads)
+        if (lc < heads)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < VEC; j += 4)
-                    *reinterpret_cast<f32x4*>(&lds_o[wave][c][4 * VEC * g + VEC * i + j]) =
+                    *reinterpret_cast<f32x4*>(&lds_o[wave][lc][4 * VEC * lg + VEC * i + j]) =
                         f32x4{o[n][j][i], o[n][j + 1][i], o[n][j + 2][i], o[n][j + 3][i]};
         __syncthreads();
-        for (int it = tid; it < heads * (W / 4); it += 64 * kWaves) {
+        for (int it = late; it < heads * (W / 4); it += 64 * kWaves) {
             const int h = it / (W / 4), d = (it & (W / 4 - 1)) * 4, at = 128 * n + d;
             if (!FULL && at >= a.dim) continue;
             f32x4 sum = {0, 0, 0, 0};
