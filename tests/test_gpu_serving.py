@@ -231,6 +231,29 @@ def test_e4m3_cache_rounds_to_nearest_even_and_saturates():
         assert torch.equal(got[ok], want[ok])
 
 
+def test_rope_of_more_tokens_than_a_grid_axis_takes():
+    # past 2^24 workgroups of 256 threads: the rows of a small call, over and over
+    P, n = 4096, 4099
+    g = np.random.default_rng(8)
+    q, k, v = (normal(g, (P, 8), "bf16") for _ in range(3))
+    pos = i32(g.integers(-1, 100000, P))
+    plan = hts.rope_plan(8, device=DEV)
+    want_q, want_k = hts.rope(q.clone(), k.clone(), pos, plan)
+    T = n * P
+    qq, kk, pp = q.repeat(n, 1), k.repeat(n, 1), pos.repeat(n)
+    hts.rope(qq, kk, pp, plan)
+    assert torch.equal(qq.view(n, P, 8), want_q.expand(n, P, 8)) and torch.equal(kk.view(n, P, 8), want_k.expand(n, P, 8))
+    # and into a cache of as many tokens, where a skipped token leaves its place as it was
+    cache = hts.kv_cache(T // 1024, 1024, 1, 8, torch.bfloat16, DEV)
+    qq = q.repeat(n, 1)
+    hts.rope_cache(qq, k.repeat(n, 1), v.repeat(n, 1), pp, torch.arange(T, device=DEV), plan, cache)
+    live = (pos >= 0)[:, None]
+    zero = torch.zeros_like(k)
+    assert torch.equal(qq.view(n, P, 8), want_q.expand(n, P, 8))
+    assert torch.equal(cache.k.view(n, P, 8), torch.where(live, want_k, zero).expand(n, P, 8))
+    assert torch.equal(cache.v.view(n, P, 8), torch.where(live, v, zero).expand(n, P, 8))
+
+
 # ---- attention -------------------------------------------------------------
 
 ATTN = [  # dim, q heads, k heads, page, order, cache, window, lengths
@@ -556,6 +579,31 @@ def test_steps_on_another_stream():
     assert torch.equal(r, r2) and torch.equal(y, y2)
 
 
+def test_paged_attn_joins_more_heads_than_a_grid_axis_takes():
+    # 4096 requests of 4352 heads: the join takes 2.2 million workgroups; the one request that is cut lies past 2^21
+    B, hk, hq, dim, page, long = 4096, 128, 4352, 128, 16, 4090
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    c = hts.KVCache(*(torch.randn((8, page, hk, dim), generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2)))
+    n = torch.ones(B, dtype=torch.int32, device=DEV)
+    n[long] = 134400
+    width = 134400 // page
+    table = torch.randint(0, 8, (B, width), generator=g, device=DEV, dtype=torch.int32)
+    q = torch.randn((B, hq * dim), generator=g, device=DEV, dtype=torch.bfloat16)
+    assert c.workspace_bytes(B, hq, width) > 0
+    out = hts.paged_attn(q, c, table, n)
+    rest = torch.arange(B, device=DEV) != long
+    # a request of one token: its value, in every head of the group
+    v = c.v[table[:, 0].long(), 0]
+    for b in range(0, B, 512):
+        want = v[b:b + 512, :, None].expand(-1, hk, hq // hk, dim).reshape(512, -1)
+        assert torch.equal(out[b:b + 512][rest[b:b + 512]], want[rest[b:b + 512]])
+    # the long one: the same call by itself, cut at other places (32-bit sums in another order, one rounding each)
+    alone = hts.paged_attn(q[long:long + 1], c, table[long:long + 1], n[long:long + 1])
+    assert torch.all((out[long] - alone[0]).abs().float() <= 2.0 ** -7 * alone[0].abs().float() + 2.0 ** -10)
+    assert bool((out[long] != 0).any())
+
+
 # ---- norm ------------------------------------------------------------------
 
 NORM = [  # post, pre, gate, act, scale, residual
@@ -597,6 +645,21 @@ def test_residual_norm(M, N, post, pre, gate, act, scale, res, dtype):
     r2, x2 = r.clone(), x.clone()
     hts.residual_norm(x2, r2, norms["post"], norms["pre"], gt, act, scale, residual_out=r2, out=x2)
     assert torch.equal(r2, got_r) and torch.equal(x2, got_y)
+
+
+@pytest.mark.parametrize("N,n", [(8, 65537), (264, 513)])
+def test_residual_norm_of_more_rows_than_a_grid_axis_takes(N, n):
+    # 2^28 rows of 16 lanes and more are 2^32 threads; 2^21 rows of a workgroup each are an axis
+    P = 4096
+    g = np.random.default_rng(N)
+    x, w = normal(g, (P, N), "bf16"), hts.Norm("layer", normal(g, (N,), "bf16"))
+    want = hts.residual_norm(x, None, pre=w, keep_residual=False)[1]
+    big = x.repeat(n, 1)
+    assert big.shape[0] > (2 ** 28 if N == 8 else 2 ** 21)
+    hts.residual_norm(big, None, pre=w, keep_residual=False, out=big)
+    for i in range(0, n, 4096):
+        part = big[i * P:(i + 4096) * P].view(-1, P, N)
+        assert torch.equal(part, want.expand_as(part))
 
 
 def test_residual_norm_parts():

@@ -276,3 +276,32 @@ def test_shorter_products_respect_wait_states(tmp_path, monkeypatch):
         out = iw._regs(iw._ops(first)[1][0])
         _, a, b, acc = iw._ops(second)[1][:4]
         assert not out & (iw._regs(a) | iw._regs(b)) and (iw._regs(acc) == out or not iw._regs(acc) & out), (first, second)
+
+
+def test_wide_grids_fit_their_axes(tmp_path):
+    # workgroups of a launch in two axes: every one of n is there, an axis holds fewer than 2^32 threads of 1024 a group
+    import os
+    import subprocess
+    from tile_gemm_amd import build as hb
+    try:
+        hipcc = hb.hipcc()
+    except RuntimeError:
+        pytest.skip("hipcc not available")
+    src = tmp_path / "grid.cpp"
+    src.write_text("""#include <cstdio>
+#include "serve_internal.h"
+int main() {
+    for (long long n : {1ll, 255ll, (1ll << 21) - 1, 1ll << 21, (1ll << 21) + 1, 1ll << 24, (1ll << 31) - 1}) {
+        const hts::WideGrid w = hts::wide_grid(n);
+        const long long x = w.x, rest = w.rest;
+        const bool ok = x * 1024 < (1ll << 32) && rest <= 65535 && x * rest >= n && (rest - 1) * x < n && (rest == 1 || x == hts::kGridX);
+        std::printf("%lld %s\\n", n, ok ? "ok" : "bad");
+    }
+}
+""")
+    flags = [f for f in hb.COMMON if f.startswith("-I") or f.startswith("-std")]
+    subprocess.run([hipcc, *flags, "-x", "hip", f"--offload-arch={hb.ARCH}", "--cuda-host-only", "-c", str(src), "-o", str(tmp_path / "g.o")],
+                   check=True, capture_output=True)
+    subprocess.run([hipcc, str(tmp_path / "g.o"), "-o", str(tmp_path / "g")], check=True, capture_output=True)
+    got = subprocess.run([str(tmp_path / "g")], capture_output=True, text=True, check=True).stdout.split()
+    assert len(got) == 14 and set(got[1::2]) == {"ok"}, got

@@ -537,7 +537,7 @@ constexpr int kFlatThreads = 256, kFlatParts = 4;
 template <typename T>
 __global__ __launch_bounds__(kFlatThreads) void join_flat_kernel(AttnArgs a) {
     const int quads = a.dim / 4, per = kFlatThreads / quads, row = threadIdx.x / quads;
-    const int64_t i = (int64_t)blockIdx.x * per + row;
+    const int64_t i = (blockIdx.y * kGridX + blockIdx.x) * per + row;
     if (row >= per || i >= (int64_t)a.B * a.q_heads) return;
     const int b = (int)(i / a.q_heads), h = (int)(i - (int64_t)b * a.q_heads), d = (threadIdx.x - row * quads) * 4;
     const uint2 plan = a.plan[b];
@@ -669,7 +669,8 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
         join_kernel<T><<<dim3((unsigned)a.B, (unsigned)a.q_heads), dim3(kJoinThreads), 0, s>>>(a);
     } else {
         const int64_t per = kFlatThreads / (a.dim / 4);
-        join_flat_kernel<T><<<dim3((unsigned)((heads + per - 1) / per)), dim3(kFlatThreads), 0, s>>>(a);
+        const WideGrid wide = wide_grid((heads + per - 1) / per);
+        join_flat_kernel<T><<<dim3(wide.x, wide.rest), dim3(kFlatThreads), 0, s>>>(a);
     }
     return hipGetLastError();
 }

@@ -46,8 +46,9 @@ template <typename T, bool R32, int LANES, int CH>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormArgs a) {
     __shared__ float sums[4][16];        // a layer norm takes two sums, and there are two norms
     const int per_row = LANES ? LANES : blockDim.x, me = LANES ? threadIdx.x % LANES : threadIdx.x;
-    const int64_t m = LANES ? (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES : blockIdx.x;
-    if (LANES && m >= a.M) return;       // rows of one wave end apart: their shuffles stay within a row
+    const int64_t group = blockIdx.y * kGridX + blockIdx.x;
+    const int64_t m = LANES ? group * (256 / LANES) + threadIdx.x / LANES : group;
+    if (m >= a.M) return;                // rows of one wave end apart: their shuffles stay within a row
     float x[CH][8];
     // entry of chunk c; past the row's end a chunk holds zeros and stays out of the sums
     const auto col = [&](int c) { return (c * per_row + me) * 8; };
@@ -166,9 +167,12 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void residual_norm_kernel(NormA
 template <typename T, bool R32>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
     const int chunks = a.N / 8;
-    const auto rows_of = [&](int per) { return dim3((unsigned)((a.M + per - 1) / per)); };
+    const auto rows_of = [&](int per) {
+        const WideGrid wide = wide_grid((a.M + per - 1) / per);
+        return dim3(wide.x, wide.rest);
+    };
     const auto threads = [&](int ch) { return dim3((unsigned)(((chunks + ch - 1) / ch + 63) / 64 * 64)); };
-    const dim3 grid((unsigned)a.M);
+    const dim3 grid = rows_of(1);
     // Lanes of a wave for short rows (65536 x 128: 11.6 us against 22.1 with a workgroup of one wave each, 65536 x 256:
     // 21.6 against 23.0).  Else one chunk per thread while the rows are few, for the shortest chain (1 x 4096:
     // 2.8 us against 3.5 with two; 2048 x 4096: 12.1 against 12.6), two for many (16384 x 4096 with gate and layer

@@ -47,7 +47,8 @@ template <int V> __device__ __forceinline__ void store_e4m3(uint8_t* p, const fl
 template <typename T, int LAYOUT, int P, bool C8>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     __shared__ float cs[128], sn[128];
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.z * kGridX + blockIdx.x;
+    if (t >= a.T) return;
     const int pos = a.positions[t];
     if (pos < 0) return;
     const int half = a.rot / 2;
@@ -154,7 +155,8 @@ hipError_t launch(const RopeArgs& a, hipStream_t s) {
     // one workgroup per token; where that leaves CUs idle, up to 4 that share the token's items (each makes the angles)
     const int64_t items = ((int64_t)(a.q_heads + a.k_heads) * (a.dim / 16) + (int64_t)a.k_heads * (a.dim / 8)) / kThreads;
     const int64_t share = a.T >= 256 ? 1 : items < 1 ? 1 : items > 4 ? 4 : items;
-    const dim3 grid((unsigned)a.T, (unsigned)share), block(kThreads);
+    const WideGrid wide = wide_grid(a.T);
+    const dim3 grid(wide.x, (unsigned)share, wide.rest), block(kThreads);
     if (a.layout == HTS_ROPE_INTERLEAVED) {
         if (a.cache8) rope_kernel<T, HTS_ROPE_INTERLEAVED, 4, true><<<grid, block, 0, s>>>(a);
         else rope_kernel<T, HTS_ROPE_INTERLEAVED, 4, false><<<grid, block, 0, s>>>(a);

@@ -8,6 +8,16 @@
 
 namespace hts {
 
+// Workgroups of a launch in two grid axes, n below 2^31 or so: HIP takes fewer than 2^32 threads in one, that is 2^24 of 256
+// or 2^22 of 1024.  Workgroup i is (i % kGridX, i / kGridX), and those past n return.
+constexpr int64_t kGridX = int64_t(1) << 21;
+struct WideGrid {
+    unsigned x, rest;
+};
+inline WideGrid wide_grid(int64_t n) {
+    return n <= kGridX ? WideGrid{(unsigned)n, 1u} : WideGrid{(unsigned)kGridX, (unsigned)((n + kGridX - 1) / kGridX)};
+}
+
 // hts_kv_step keeps one prefix-sum entry of each kind per request in LDS.
 constexpr int kMaxStepRequests = 4096;
 struct KvStepArgs {
