@@ -361,6 +361,15 @@ def test_paged_attn(dim, hq, hk, page, order, cache, window, lengths, dtype):
     _check_attn(q, c, table, width, lengths, hq, window, scale, q2, None, dtype)
 
 
+def test_paged_attn_of_one_cache_head_in_either_order():
+    # the same memory in "token" and in "head" order (they differ in a stride that one head does not use): the same bits
+    lengths = [9000, 70, 0, 5000]
+    q, c, table, width = _attn_case(128, 8, 1, 16, "token", "same", lengths, "bf16", 21)
+    other = hts.KVCache(*(x.as_strided(x.shape, (x.stride(0), x.stride(1), 16 * 128, 1)) for x in (c.k, c.v)))
+    args = i32(table)[:, :width], i32(lengths)
+    assert torch.equal(hts.paged_attn(q, c, *args), hts.paged_attn(q, other, *args))
+
+
 def test_paged_attn_leaves_out_what_no_page_holds():
     # entries of -1, ids past the cache and lengths past the table (and negative) within the requests
     lengths = [200, 90, 33, 64]

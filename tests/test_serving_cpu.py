@@ -113,6 +113,18 @@ def test_cache_descriptions_that_are_taken():
         assert hts.lib().hts_paged_attn_workspace(4, 32, by(kv(**change)), 8, 0, by(n)) == 0, change
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [hts.HTS_BF16, hts.HTS_FP8_E4M3])
+def test_unused_strides_change_nothing(dim, dtype):
+    # one cache head, or one page: whatever stands in that axis's stride, the same memory is divided alike
+    def bytes_of(**change):
+        d = kv(**{**dict(heads=1, dim=dim, dtype=dtype, token_stride=dim, page_stride=16 * dim, head_stride=dim), **change})
+        return hts.hts_paged_attn_workspace(64, 16, d, 512)
+    assert bytes_of() > 0
+    assert len({bytes_of(head_stride=s) for s in (dim, 16 * dim, 0, -8, 3, 2 ** 40)}) == 1
+    assert len({bytes_of(pages=1, page_stride=s) for s in (16 * dim, 0, -8, 3, 2 ** 40)}) == 1
+
+
 @pytest.mark.parametrize("rule,factor,context", [("plain", 1.0, 0.0), ("plain", 3.0, 0.0), ("linear", 4.0, 0.0), ("base", 8.0, 0.0),
                                                  ("ramp", 8.0, 4096.0), ("ramp_pairs", 16.0, 4096.0),
                                                  ("ramp_pairs", 2.5, 100.0)])

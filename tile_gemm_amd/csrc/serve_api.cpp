@@ -117,9 +117,12 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     // on an 8-bit cache: 113.9 and 112.4).  Fewer stream as fast where each has long stretches to itself, and leave
     // fewer parts: one a CU for heads above 128 (16 requests up to 8192, 16/4 heads of 256: 57.7 us with 256 runs, 59.4
     // with 512), two where a page holds a head's tokens one after another (256 requests up to 2048, 32/8 heads, pages
-    // of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209).
-    const int64_t runs = kv->dim > 128                        ? 256
-                         : kv->head_stride > kv->token_stride ? 512
+    // of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209), as it does where there is one
+    // head, whose stride is not used (64 up to 8191, 16/1 heads: 36.1 us with 512, 40.1 with 768; 4 up to 131072, 8/1: 39.9
+    // and 42.0; 32 up to 4096, 4/1: 14.8 and 14.7).
+    const bool in_a_row = kv->heads == 1 || kv->head_stride > kv->token_stride;
+    const int64_t runs = kv->dim > 128 ? 256
+                         : in_a_row    ? 512
                          : kv->dim < 128 && kv->dtype != HTS_FP8_E4M3 ? 1024
                                                                       : 768;
     p.target = (int32_t)std::max<int64_t>(1, runs / rows);
