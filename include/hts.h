@@ -385,6 +385,17 @@ hts_status hts_rope_cache(const hts_rope_desc* d, const double* turns, int64_t T
                           void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
                           void* stream);
 
+/* Device, asynchronous.  hts_rope_cache with a row for each of B requests in place of each token, for steps that
+ * add at most one token to a request: row b belongs to request b, whose token in the step is starts[b] (device
+ * int32[B + 1], as hts_kv_step writes them; positions and slots have `tokens` entries, one at least where B > 0).  A row
+ * whose request adds no token is skipped whole, as is one whose token's position is negative.  Where a request adds more
+ * than one, or its token lies past `tokens`, the rotated entries of its q become NaN and nothing of it is cached. */
+hts_status hts_rope_cache_rows(const hts_rope_desc* d, const double* turns, int64_t B, const int32_t* starts,
+                               int64_t tokens, const int32_t* positions, const int64_t* slots, const void* Q, int64_t ldq,
+                               void* Q_out, int64_t ldqo, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                               const hts_kv_desc* kv, void* k_cache, void* v_cache, const float* k_scale,
+                               const float* v_scale, void* stream);
+
 /* Device, asynchronous.  Attention of one new token per request over the paged cache.  For request
  * b and query head h (cache head h / (q_heads / kv->heads)), over the tokens t in
  * [max(0, L - window), L), L = lengths[b] (device int32[B], clamped to 0 .. width*page; window 0 =

@@ -200,6 +200,65 @@ def test_padding_rows_change_nothing():
         assert torch.equal(k, layer.cache.k)
 
 
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_paused_requests(graph):
+    # requests that add no token in some steps, in the middle of the batch: each one's outputs are those of its own tokens
+    model = Model(torch.bfloat16, seed=5)
+    B, steps, width = 5, 24, 4
+    active = np.random.default_rng(1).random((steps, B)) < 0.6
+    active[0], active[1], active[:, 3] = True, [1, 0, 1, 0, 1], False       # request 3 has no token at all
+    g = torch.Generator(device=DEV)
+    g.manual_seed(10)
+    xs = torch.randn((steps, B, HID), generator=g, device=DEV).bfloat16()
+    free = torch.arange(64, device=DEV).int()
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    cached, added, head = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (B, B, 1))
+    x = torch.zeros((B, HID), dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        st = hts.kv_step(cached, added, free, table, PAGE, B, free_head=head)
+        y = model.forward(x, st, table)
+        cached.copy_(st.lengths)
+        head.copy_(st.head)
+        return y
+    if graph:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()                                       # nothing is added
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            y = step()
+    outs = []
+    for i in range(steps):
+        x.copy_(xs[i])
+        added.copy_(torch.from_numpy(active[i].astype(np.int32)))
+        if graph:
+            gr.replay()
+            torch.cuda.synchronize()
+        else:
+            y = step()
+        outs.append(y.clone())
+    got = torch.stack(outs).double().cpu().numpy()
+    assert cached.tolist() == active.sum(0).tolist()
+    for b in (0, 1, 2, 4):
+        mine = active[:, b]
+        want = model.reference(xs[:, b].double().cpu().numpy()[mine])
+        err = np.linalg.norm(got[mine, b] - want, axis=1) / np.linalg.norm(want, axis=1)
+        say(f"[decode] paused, request {b} of {mine.sum()} tokens: relative error {err.max():.4f}")
+        assert err.max() <= 24 * 2.0 ** -9               # as in test_generation_matches_the_model_in_64_bits
+
+
+def test_a_request_that_adds_two_tokens_is_not_decoded_silently():
+    model = Model(torch.bfloat16, seed=5)
+    free, table = torch.arange(64, device=DEV).int(), torch.full((3, 2), -1, dtype=torch.int32, device=DEV)
+    cached, added = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 0, 0], [1, 2, 0]))
+    x = torch.ones((3, HID), dtype=torch.bfloat16, device=DEV)
+    y = model.forward(x, hts.kv_step(cached, added, free, table, PAGE, 3), table)
+    assert bool(torch.isnan(y[1]).all()) and bool(torch.isfinite(y[0]).all())
+
+
 def test_block_refuses_shapes_that_do_not_fit():
     model = Model(torch.bfloat16, seed=6)
     layer, st = model.layers[0], hts.KVStep.buffers(2, 2, DEV)

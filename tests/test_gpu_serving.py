@@ -231,6 +231,35 @@ def test_e4m3_cache_rounds_to_nearest_even_and_saturates():
         assert torch.equal(got[ok], want[ok])
 
 
+@pytest.mark.parametrize("cache_dtype", ["bf16", "fp8"])
+def test_rope_cache_of_a_row_per_request(cache_dtype):
+    # requests that add no token, one, two, one past the capacity: rows of the second kind as if token by token
+    dim, hq, hk, page = 64, 4, 2, 16
+    g = np.random.default_rng(9)
+    starts = [0, 1, 1, 2, 3, 5, 6, 6, 7, 8]               # requests 1 and 6 add none, 4 two, the last's token is past 7
+    live, none, lost = [0, 2, 3, 5, 7], [1, 6], [4, 8]
+    B, tokens = len(starts) - 1, 7
+    q, k, v = (normal(g, (B, h * dim), "bf16") for h in (hq, hk, hk))
+    pos, slots = i32([5, 9, -1, 100, 101, 77, 3]), torch.tensor([40, 3, 17, 18, 19, 60, -1], device=DEV)
+    plan = hts.rope_plan(dim, 32, device=DEV)
+    caches = [hts.kv_cache(4, page, hk, dim, TORCH[cache_dtype], DEV) for _ in range(2)]
+    out = torch.full_like(q, 3.0)
+    hts.rope_cache(q, k, v, pos, slots, plan, caches[0], q_out=out, starts=i32(starts))
+    at = torch.tensor([starts[b] for b in live], device=DEV)
+    want = torch.full_like(q, 3.0)
+    rows = torch.tensor(live, device=DEV)
+    part = torch.full((len(live), hq * dim), 3.0, dtype=q.dtype, device=DEV)
+    hts.rope_cache(q[rows], k[rows], v[rows], pos[at], slots[at], plan, caches[1], q_out=part)
+    want[rows] = part
+    assert torch.equal(out[rows], want[rows]) and torch.all(out[none] == 3.0) and torch.all(out[3] == 3.0)
+    for a, b in zip((caches[0].k, caches[0].v), (caches[1].k, caches[1].v)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and bool((a.float() != 0).any())
+    assert bool(torch.isnan(out[lost].view(2, hq, dim)[..., :32]).all())
+    for bad in (i32(starts[:-1]), i32([]), i32(starts).long()):
+        with pytest.raises(hts.HTSError):
+            hts.rope_cache(q, k, v, pos, slots, plan, caches[0], q_out=out, starts=bad)
+
+
 def test_rope_of_more_tokens_than_a_grid_axis_takes():
     # past 2^24 workgroups of 256 threads: the rows of a small call, over and over
     P, n = 4096, 4099

@@ -92,6 +92,20 @@ def test_rope_refuses():
     assert rope_cache(T=0, slots=None, kc=None) == 0
 
 
+def test_rope_cache_rows_refuses():
+    def rows(desc=None, cache=None, **k):
+        a = dict(turns=A16, B=4, starts=A16, tokens=4, positions=A16, slots=A16, Q=A16, ldq=4096, Qo=A16, ldqo=4096, K=A16,
+                 ldk=1024, V=A16, ldv=1024, kv=by(cache or kv()), kc=0x100000, vc=0x200000, ks=None, vs=None)
+        a.update(k)
+        return hts.lib().hts_rope_cache_rows(by(desc or rope_desc()), *a.values(), None)
+    for change, status in ((dict(B=-1), 3), (dict(B=2 ** 31), 3), (dict(starts=None), 1), (dict(starts=A2), 4), (dict(tokens=0), 3),
+                           (dict(tokens=-1), 3), (dict(tokens=2 ** 31), 3), (dict(positions=None), 1), (dict(slots=A4), 4),
+                           (dict(Q=None), 1), (dict(ldqo=4104), 1), (dict(V=None), 1), (dict(vc=0x100000), 1), (dict(kv=None), 1)):
+        assert rows(**change) == status, change
+    assert rows(rope_desc(rot=12)) == 7 and rows(cache=kv(heads=4)) == 3
+    assert rows(B=0, tokens=0, starts=None, positions=None, slots=None, kc=None) == 0
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(pages=0), 3), (dict(pages=2 ** 31), 3), (dict(page=8), 7), (dict(page=48), 7), (dict(heads=0), 3),
     (dict(dim=4), 7), (dict(dim=260), 7), (dict(dtype=hts.HTS_F32), 2), (dict(dtype=9), 2), (dict(head_stride=0), 3),

@@ -104,6 +104,9 @@ _SIGS = {
                                 _I64, _VP]),
     "hts_rope_cache": (ctypes.c_int, [ctypes.POINTER(hts_rope_desc), _VP, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP,
                                       _I64, _VP, _I64, ctypes.POINTER(hts_kv_desc), _VP, _VP, _VP, _VP, _VP]),
+    "hts_rope_cache_rows": (ctypes.c_int, [ctypes.POINTER(hts_rope_desc), _VP, _I64, _VP, _I64, _VP, _VP, _VP, _I64, _VP,
+                                           _I64, _VP, _I64, _VP, _I64, ctypes.POINTER(hts_kv_desc), _VP, _VP, _VP, _VP,
+                                           _VP]),
     "hts_paged_attn": (ctypes.c_int, [_I32, _I64, _I32, ctypes.POINTER(hts_kv_desc), _VP, _I64, _VP, _VP, _VP, _VP,
                                       _VP, _I64, _I64, _VP, ctypes.c_float, _I64, _VP, _I64, _VP, _VP,
                                       ctypes.c_size_t, _VP]),
@@ -323,6 +326,14 @@ def hts_rope_cache(desc: hts_rope_desc, turns, positions, slots, Q, Q_out, K, V,
                                 _ptr(Q), _ld(Q), _ptr(Q_out), _ld(Q_out), _ptr(K), _ld(K), _ptr(V), _ld(V),
                                 ctypes.byref(kv), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                 _stream(stream)))
+
+
+def hts_rope_cache_rows(desc: hts_rope_desc, turns, starts, positions, slots, Q, Q_out, K, V, kv: hts_kv_desc, k_cache,
+                        v_cache, k_scale=None, v_scale=None, stream=None) -> None:
+    _check(lib().hts_rope_cache_rows(ctypes.byref(desc), _ptr(turns), starts.numel() - 1, _ptr(starts), positions.numel(),
+                                     _ptr(positions), _ptr(slots), _ptr(Q), _ld(Q), _ptr(Q_out), _ld(Q_out), _ptr(K),
+                                     _ld(K), _ptr(V), _ld(V), ctypes.byref(kv), _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(k_scale), _ptr(v_scale), _stream(stream)))
 
 
 def hts_paged_attn_workspace(B: int, q_heads: int, kv: hts_kv_desc, width: int, window: int = 0) -> int:

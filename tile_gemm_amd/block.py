@@ -120,20 +120,21 @@ class Layer:
 
 def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step: KVStep, block_table: torch.Tensor,
            plan: RopePlan, bufs: Optional[Dict[str, torch.Tensor]] = None):
-    """One block on one new token per request: x [B, hidden], the output of the block before (its MLP, not yet
-    added) with that block's residual stream, or the embedding with residual None.  Returns (x, residual) for
+    """One block on one new token per request: row b of x [B, hidden] is request b's, the output of the block before
+    (its MLP, not yet added) with that block's residual stream, or the embedding with residual None.  Returns (x, residual) for
     the next block: the MLP's output and the stream it is to be added to.  The layer's post_mlp_norm, gate
     and scale are applied here, so that the next block only adds: give the last block's pair to
     residual_norm(x, residual, pre=final_norm).
 
-    step and block_table come from kv_step with one token added per request (its positions and slots; padding
-    rows behind the last request are carried along and change no cache entry)."""
+    step and block_table come from kv_step with B tokens of capacity and at most one token added to a request.  The row
+    of a request that adds none (padding, paused or finished, wherever it stands) is carried along and changes no
+    cache entry; what comes out in it means nothing.  A request that adds more than one gets NaN in its row."""
     w, B = layer.weights, x.shape[0]
     if x.dim() != 2 or x.shape[1] != layer.hidden:
         raise HTSError(3, f"x has shape {tuple(x.shape)}, the block's hidden size is {layer.hidden}")
     if x.dtype != w["q"].dtype:
         raise HTSError(2, f"x has type {x.dtype}, the block's weights {w['q'].dtype}")
-    if step.positions.numel() != B or step.lengths.numel() != B:
+    if step.positions.numel() != B or step.lengths.numel() != B or step.starts.numel() != B + 1:
         raise HTSError(3, f"x has {B} rows, the step {step.lengths.numel()} requests and {step.positions.numel()} tokens")
     if bufs is None:
         bufs = buffers(B, w, x.dtype, x.device)
@@ -141,7 +142,7 @@ def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step
     r, y = residual_norm(x, residual, pre=layer.input_norm)
     for name in ("q", "k", "v"):
         _linear(y, w[name], bufs[name])
-    rope_cache(bufs["q"], bufs["k"], bufs["v"], step.positions, step.slots, plan, layer.cache)
+    rope_cache(bufs["q"], bufs["k"], bufs["v"], step.positions, step.slots, plan, layer.cache, starts=step.starts)
     a = paged_attn(bufs["q"], layer.cache, block_table, step.lengths, layer.attn_scale, layer.window)
     _linear(a, w["o"], bufs["o"])
     r, y = residual_norm(bufs["o"], r, post=layer.post_attn_norm, pre=layer.mlp_norm, gate=layer.attn_gate,

@@ -49,21 +49,29 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     __shared__ float cs[128], sn[128];
     const int64_t t = blockIdx.z * kGridX + blockIdx.x;
     if (t >= a.T) return;
-    const int pos = a.positions[t];
+    int64_t token = t;
+    bool lost = false;                  // the row's request adds more than one token, or one that is not there
+    if (a.starts) {
+        const int first = a.starts[t], end = a.starts[t + 1];
+        if (first < 0 || first >= end) return;
+        lost = end - first > 1 || first >= a.tokens;
+        token = lost ? 0 : first;
+    }
+    const int pos = lost ? 0 : a.positions[token];
     if (pos < 0) return;
     const int half = a.rot / 2;
     if ((int)threadIdx.x < half) {
         double turn = (double)pos * a.turns[threadIdx.x];
         turn -= rint(turn);
         float s, c;
-        sincospif(2.0f * (float)turn, &s, &c);
+        sincospif(lost ? __builtin_nanf("") : 2.0f * (float)turn, &s, &c);
         cs[threadIdx.x] = c * a.magnitude;
         sn[threadIdx.x] = s * a.magnitude;
     }
     int64_t at = -1;                    // the token's place in the cache
     if (a.slots) {
-        const int64_t slot = a.slots[t];
-        if (slot >= 0 && slot < a.n_slots)
+        const int64_t slot = a.slots[token];
+        if (slot >= 0 && slot < a.n_slots && !lost)
             at = (slot >> a.page_shift) * a.page_stride + (slot & ((1 << a.page_shift) - 1)) * a.token_stride;
     }
     // items: all q heads, then all k heads, then v in chunks of 8

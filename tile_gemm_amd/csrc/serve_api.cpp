@@ -178,6 +178,66 @@ hts::RopeArgs rope_args(const hts_rope_desc* d, const double* turns, int64_t T, 
     return a;
 }
 
+// hts_rope_cache of T tokens, or with `starts` of T requests whose tokens lie among `tokens`.
+hts_status rope_cache(const hts_rope_desc* d, const double* turns, int64_t T, const int32_t* starts, int64_t tokens,
+                      const int32_t* positions, const int64_t* slots, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo,
+                      const void* K, int64_t ldk, const void* V, int64_t ldv, const hts_kv_desc* kv, void* k_cache,
+                      void* v_cache, const float* k_scale, const float* v_scale, void* stream) {
+    hts_status st = check_rope(d, turns, T, positions);
+    if (st) return st;
+    uint64_t span = 0;
+    if ((st = check_kv(kv, d->dtype, k_scale, v_scale, &span))) return st;
+    if (kv->dim != d->dim || kv->heads != d->k_heads)
+        return fail(HTS_ERR_SHAPE, "the cache holds %d heads of %d, the step %d of %d", kv->heads, kv->dim, d->k_heads,
+                    d->dim);
+    if (T == 0) return ok();
+    const int64_t nq = (int64_t)d->q_heads * d->dim, nk = (int64_t)d->k_heads * d->dim;
+    if ((st = check_matrix(Q, ldq, nq, "Q", "ldq")) || (st = check_matrix(Q_out, ldqo, nq, "Q_out", "ldqo")) ||
+        (st = check_matrix(K, ldk, nk, "K", "ldk")) || (st = check_matrix(V, ldv, nk, "V", "ldv")) ||
+        (st = check_ptr(k_cache, "k_cache")) || (st = check_ptr(v_cache, "v_cache")) ||
+        (st = check_aligned(slots, 8, "slots")))
+        return st;
+    if (k_cache == v_cache) return fail(HTS_ERR_INVALID_ARG, "k_cache and v_cache are one buffer");
+    if (nq && Q_out == Q && ldqo != ldq)
+        return fail(HTS_ERR_INVALID_ARG, "in place, input and output have one leading dimension");
+    const int es = kv_bytes(kv);
+    if (debug_mode() &&
+        ((st = debug_range(turns, 4 * (uint64_t)d->rot, "turns")) ||
+         (st = debug_range(positions, 4 * (uint64_t)tokens, "positions")) ||
+         (st = debug_range(slots, 8 * (uint64_t)tokens, "slots")) ||
+         (starts && (st = debug_range(starts, 4 * ((uint64_t)T + 1), "starts"))) ||
+         (nq && ((st = debug_range(Q, block_bytes(T, nq, ldq, 2), "Q")) ||
+                 (st = debug_range(Q_out, block_bytes(T, nq, ldqo, 2), "Q_out")))) ||
+         (st = debug_range(K, block_bytes(T, nk, ldk, 2), "K")) || (st = debug_range(V, block_bytes(T, nk, ldv, 2), "V")) ||
+         (st = debug_range(k_cache, span * es, "k_cache")) || (st = debug_range(v_cache, span * es, "v_cache")) ||
+         (st = debug_range(k_scale, 4 * (uint64_t)kv->heads, "k_scale")) ||
+         (st = debug_range(v_scale, 4 * (uint64_t)kv->heads, "v_scale"))))
+        return st;
+    hts::RopeArgs a = rope_args(d, turns, T, positions);
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.ldq = ldq;
+    a.Qo = static_cast<uint16_t*>(Q_out);
+    a.ldqo = ldqo;
+    a.K = static_cast<const uint16_t*>(K);
+    a.ldk = ldk;
+    a.V = static_cast<const uint16_t*>(V);
+    a.ldv = ldv;
+    a.slots = slots;
+    a.starts = starts;
+    a.tokens = tokens;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.n_slots = kv->pages * kv->page;
+    a.cache8 = kv->dtype == HTS_FP8_E4M3;
+    a.page_shift = log2i(kv->page);
+    a.page_stride = kv->page_stride;
+    a.token_stride = kv->token_stride;
+    a.head_stride = kv->head_stride;
+    return hip_status(hts::launch_rope(a, static_cast<hipStream_t>(stream)), "rotary kernel launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -319,55 +379,23 @@ hts_status hts_rope_cache(const hts_rope_desc* d, const double* turns, int64_t T
                           const int64_t* slots, const void* Q, int64_t ldq, void* Q_out, int64_t ldqo, const void* K,
                           int64_t ldk, const void* V, int64_t ldv, const hts_kv_desc* kv, void* k_cache, void* v_cache,
                           const float* k_scale, const float* v_scale, void* stream) {
-    hts_status st = check_rope(d, turns, T, positions);
-    if (st) return st;
-    uint64_t span = 0;
-    if ((st = check_kv(kv, d->dtype, k_scale, v_scale, &span))) return st;
-    if (kv->dim != d->dim || kv->heads != d->k_heads)
-        return fail(HTS_ERR_SHAPE, "the cache holds %d heads of %d, the step %d of %d", kv->heads, kv->dim, d->k_heads,
-                    d->dim);
-    if (T == 0) return ok();
-    const int64_t nq = (int64_t)d->q_heads * d->dim, nk = (int64_t)d->k_heads * d->dim;
-    if ((st = check_matrix(Q, ldq, nq, "Q", "ldq")) || (st = check_matrix(Q_out, ldqo, nq, "Q_out", "ldqo")) ||
-        (st = check_matrix(K, ldk, nk, "K", "ldk")) || (st = check_matrix(V, ldv, nk, "V", "ldv")) ||
-        (st = check_ptr(k_cache, "k_cache")) || (st = check_ptr(v_cache, "v_cache")) ||
-        (st = check_aligned(slots, 8, "slots")))
-        return st;
-    if (k_cache == v_cache) return fail(HTS_ERR_INVALID_ARG, "k_cache and v_cache are one buffer");
-    if (nq && Q_out == Q && ldqo != ldq)
-        return fail(HTS_ERR_INVALID_ARG, "in place, input and output have one leading dimension");
-    const int es = kv_bytes(kv);
-    if (debug_mode() &&
-        ((st = debug_range(turns, 4 * (uint64_t)d->rot, "turns")) || (st = debug_range(positions, 4 * (uint64_t)T, "positions")) ||
-         (st = debug_range(slots, 8 * (uint64_t)T, "slots")) ||
-         (nq && ((st = debug_range(Q, block_bytes(T, nq, ldq, 2), "Q")) ||
-                 (st = debug_range(Q_out, block_bytes(T, nq, ldqo, 2), "Q_out")))) ||
-         (st = debug_range(K, block_bytes(T, nk, ldk, 2), "K")) || (st = debug_range(V, block_bytes(T, nk, ldv, 2), "V")) ||
-         (st = debug_range(k_cache, span * es, "k_cache")) || (st = debug_range(v_cache, span * es, "v_cache")) ||
-         (st = debug_range(k_scale, 4 * (uint64_t)kv->heads, "k_scale")) ||
-         (st = debug_range(v_scale, 4 * (uint64_t)kv->heads, "v_scale"))))
-        return st;
-    hts::RopeArgs a = rope_args(d, turns, T, positions);
-    a.Q = static_cast<const uint16_t*>(Q);
-    a.ldq = ldq;
-    a.Qo = static_cast<uint16_t*>(Q_out);
-    a.ldqo = ldqo;
-    a.K = static_cast<const uint16_t*>(K);
-    a.ldk = ldk;
-    a.V = static_cast<const uint16_t*>(V);
-    a.ldv = ldv;
-    a.slots = slots;
-    a.kc = k_cache;
-    a.vc = v_cache;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.n_slots = kv->pages * kv->page;
-    a.cache8 = kv->dtype == HTS_FP8_E4M3;
-    a.page_shift = log2i(kv->page);
-    a.page_stride = kv->page_stride;
-    a.token_stride = kv->token_stride;
-    a.head_stride = kv->head_stride;
-    return hip_status(hts::launch_rope(a, static_cast<hipStream_t>(stream)), "rotary kernel launch");
+    return rope_cache(d, turns, T, nullptr, T, positions, slots, Q, ldq, Q_out, ldqo, K, ldk, V, ldv, kv, k_cache, v_cache,
+                      k_scale, v_scale, stream);
+}
+
+hts_status hts_rope_cache_rows(const hts_rope_desc* d, const double* turns, int64_t B, const int32_t* starts,
+                               int64_t tokens, const int32_t* positions, const int64_t* slots, const void* Q, int64_t ldq,
+                               void* Q_out, int64_t ldqo, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                               const hts_kv_desc* kv, void* k_cache, void* v_cache, const float* k_scale,
+                               const float* v_scale, void* stream) {
+    if (tokens < (B > 0) || tokens >= kInt32)
+        return fail(HTS_ERR_SHAPE, "tokens=%lld is not from 1 to 2^31 - 1", (long long)tokens);
+    if (B > 0) {
+        const hts_status st = check_aligned(starts, 4, "starts");
+        if (st) return st;
+    }
+    return rope_cache(d, turns, B, starts, tokens, positions, slots, Q, ldq, Q_out, ldqo, K, ldk, V, ldv, kv, k_cache,
+                      v_cache, k_scale, v_scale, stream);
 }
 
 hts_status hts_paged_attn_workspace(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t width, int64_t window,

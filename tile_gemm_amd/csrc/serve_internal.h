@@ -45,6 +45,8 @@ struct RopeArgs {
     uint16_t *Qo, *Ko;         // Ko: nullptr where K goes to the cache
     int64_t ldq, ldqo, ldk, ldko, ldv;
     const int64_t* slots;      // nullptr: no cache
+    const int32_t* starts;     // nullptr: row t is token t; else T + 1 entries: it is request t's, whose token is starts[t]
+    int64_t tokens;            // entries of positions and slots
     void *kc, *vc;
     const float *k_scale, *v_scale;
     int64_t n_slots;

@@ -297,25 +297,37 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
 
 
 def rope_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
-               plan: RopePlan, cache: KVCache, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+               plan: RopePlan, cache: KVCache, q_out: Optional[torch.Tensor] = None, stream=None,
+               starts: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Rotate q (into q_out, or in place) and write the rotated k, and v, of token t to slot slots[t] (int64)
     of the cache.  Tokens with a negative position are skipped; tokens with a slot outside the cache are not
-    cached.  Slots must differ from one another.  Returns q_out."""
-    dev, T, dt, dim = _gpu(q, "q"), positions.numel(), q.dtype, plan.dim
+    cached.  Slots must differ from one another.  Returns q_out.
+
+    With ``starts`` (int32[B + 1], a step's) row b of q, k and v is request b's in place of token b's, for steps that
+    add at most one token to a request: a request's row takes the position and slot of its token, starts[b]; one that
+    adds none is skipped.  One that adds more, or whose token is past the step's capacity, gets NaN in q, and nothing of
+    it is cached."""
+    dev, tokens, dt, dim = _gpu(q, "q"), positions.numel(), q.dtype, plan.dim
+    entry, T, rows = _c.lib().hts_rope_cache, tokens, ()
+    if starts is not None:
+        T = starts.numel() - 1
+        if T < 0:
+            _bad("starts must have an entry for each request, and one more", 3)
+        entry, rows = _c.lib().hts_rope_cache_rows, (_vec(starts, "starts", T + 1, torch.int32, dev), tokens)
     if cache.gpu != dev:
         _bad(f"the cache is on GPU {cache.gpu}, q on GPU {dev}")
     hq, hk = _rope_heads(q, "q", dim), _rope_heads(k, "k", dim)
     nq, nk = hq * dim, hk * dim
     q_out = q if q_out is None else q_out
     ks, vs = cache.k_scale, cache.v_scale
-    args = (_rope_desc(dt, plan, hq, hk), _vec(plan.turns, "plan", plan.rot // 2, torch.float64, dev), T,
-            _vec(positions, "positions", T, torch.int32, dev), _vec(slots, "slots", T, torch.int64, dev),
+    args = (_rope_desc(dt, plan, hq, hk), _vec(plan.turns, "plan", plan.rot // 2, torch.float64, dev), T, *rows,
+            _vec(positions, "positions", tokens, torch.int32, dev), _vec(slots, "slots", tokens, torch.int64, dev),
             q.data_ptr(), _lead(q, "q", T, nq, dt, dev), q_out.data_ptr(), _lead(q_out, "q_out", T, nq, dt, dev),
             k.data_ptr(), _lead(k, "k", T, nk, dt, dev), v.data_ptr(), _lead(v, "v", T, nk, dt, dev), cache._desc,
             cache.k.data_ptr(), cache.v.data_ptr(), None if ks is None else ks.data_ptr(),
             None if vs is None else vs.data_ptr())
     with _scope(dev, stream):
-        _c._check(_c.lib().hts_rope_cache(*args, _c._current_stream(dev)))
+        _c._check(entry(*args, _c._current_stream(dev)))
     return q_out
 
 
