@@ -922,3 +922,59 @@ def test_one_page_for_all_and_for_a_whole_row():
     _check_attn(q, c, table, 80, lengths, 4, 0, 64 ** -0.5, out, None, "f16")
     # 1280 tokens that repeat 16 tokens 80 times: the attention over the 16
     assert float((out[0].float() - out[1].float()).abs().max()) <= 2.0 ** -10 * float(c.v.float().abs().max())
+
+
+@pytest.mark.parametrize("M", [1, 5])
+def test_functions_with_the_c_names_match_the_helpers(M):
+    # the marshalling under the entry points' own names; one row may come as a view with any stride between rows
+    g = np.random.default_rng(M)
+    dim, hq, hk, page, width = 64, 4, 2, 16, 3
+
+    def view(cols):
+        x = normal(g, (M, cols), "bf16")
+        return x if M > 1 else torch.as_strided(x, (1, cols), (cols + 3, 1))
+    i64 = dict(dtype=torch.int64, device=DEV)
+    # page step
+    cached, added, free = i32(g.integers(0, 20, M)), i32(np.ones(M)), i32(g.permutation(32))
+    tables = [torch.full((M, width), 31, dtype=torch.int32, device=DEV) for _ in range(2)]
+    want = hts.kv_step(cached, added, free, tables[0], page, M + 2, free_head=i32([1]))
+    got = hts.KVStep(*(torch.empty_like(x) for x in (want.lengths, want.starts, want.slots, want.positions, want.head)))
+    hts.hts_kv_step(cached, added, page, free, i32([1]), tables[1] if M > 1 else tables[1].as_strided((1, width), (1, 1)), got.lengths,
+                    got.starts, got.slots, got.positions, got.head)
+    for name in ("lengths", "starts", "slots", "positions", "head"):
+        assert torch.equal(getattr(got, name), getattr(want, name)), name
+    assert torch.equal(*tables)
+    # rotary
+    plan = hts.rope_plan(dim, 32, layout="interleaved", magnitude=1.5, device=DEV)
+    turns = hts.hts_rope_plan(hts.hts_rope_scaling(32, 0, 10000.0, 1.0, 0.0, 1.0, 32.0))
+    assert np.array_equal(turns, plan.turns.cpu().numpy())
+    desc = hts.hts_rope_desc(hts.HTS_BF16, plan.layout, dim, 32, hq, hk, 1.5, 0)
+    q, k, v = view(hq * dim), view(hk * dim), view(hk * dim)
+    pos, slots = i32(np.arange(M) * 7 + 3), torch.tensor(g.permutation(64)[:M], **i64)
+    outs = [torch.zeros((M, h * dim), dtype=torch.bfloat16, device=DEV) for h in (hq, hk, hq, hk)]
+    hts.rope(q, k, pos, plan, q_out=outs[0], k_out=outs[1])
+    hts.hts_rope(desc, plan.turns, pos, q, outs[2], k, outs[3])
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]) and bool((outs[1] != 0).any())
+    caches = [hts.kv_cache(4, page, hk, dim, torch.bfloat16, DEV) for _ in range(3)]
+    hts.rope_cache(q, k, v, pos, slots, plan, caches[0], q_out=outs[0])
+    hts.hts_rope_cache(desc, plan.turns, pos, slots, q, outs[2], k, v, caches[1].desc, caches[1].k, caches[1].v)
+    starts = torch.arange(M + 1, dtype=torch.int32, device=DEV)
+    hts.hts_rope_cache_rows(desc, plan.turns, starts, pos, slots, q, outs[1].new_empty((M, hq * dim)), k, v, caches[2].desc, caches[2].k,
+                            caches[2].v)
+    for c in caches[1:]:
+        assert torch.equal(c.k, caches[0].k) and torch.equal(c.v, caches[0].v)
+    assert torch.equal(outs[0], outs[2]) and bool((caches[0].v != 0).any())
+    # attention
+    cache, table, n = caches[0], i32(g.integers(0, 4, (M, width))), i32(g.integers(1, 48, M))
+    lse = [torch.empty((M, hq), device=DEV) for _ in range(2)]
+    want = hts.paged_attn(q, cache, table, n, scale=0.2, window=20, lse=lse[0])
+    hts.hts_paged_attn(hq, cache.desc, q, cache.k, cache.v, table, n, 0.2, outs[2], window=20, lse=lse[1])
+    assert torch.equal(outs[2], want) and torch.equal(*lse)
+    # norm: gates of a row per token and of one row
+    x, r, w = view(256), normal(g, (M, 256), "f32"), normal(g, (256,), "bf16")
+    d = hts.hts_norm_desc(hts.HTS_BF16, hts.HTS_F32, 0, 1, 0.0, 1e-5, 0.5, 1)
+    for gate in (view(256), normal(g, (256,), "bf16")):
+        want = hts.residual_norm(x, r, pre=hts.Norm("rms", w, eps=1e-5), gate=gate, gate_act="sigmoid", scale=0.5)
+        got = [torch.empty_like(r), torch.empty((M, 256), dtype=torch.bfloat16, device=DEV)]
+        hts.hts_residual_norm(d, M, 256, x, None, None, gate, r, w, None, *got)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -162,8 +162,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _ld(t: Optional[torch.Tensor]) -> int:
-    """Leading dimension: elements between rows (0: no matrix, or one row shared by all)."""
-    return t.stride(0) if t is not None and t.dim() == 2 else 0
+    """Leading dimension: elements between rows (0: no matrix, or one row shared by all).  A matrix of one row may carry
+    any stride there: it gets one that the library takes."""
+    if t is None or t.dim() != 2:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
 def _current_stream(device: int) -> int:
@@ -302,7 +305,7 @@ def hts_wanda_map(cost, n_sparse: int, tile_map, stream=None) -> None:
 def hts_kv_step(cached, added, page: int, free_pages, free_head, block_table, lengths, starts, slots, positions,
                 head_out, stream=None) -> None:
     _check(lib().hts_kv_step(cached.numel(), _ptr(cached), _ptr(added), page, _ptr(free_pages), free_pages.numel(),
-                             _ptr(free_head), _ptr(block_table), block_table.stride(0), block_table.shape[1],
+                             _ptr(free_head), _ptr(block_table), _ld(block_table), block_table.shape[1],
                              slots.numel(), _ptr(lengths), _ptr(starts), _ptr(slots), _ptr(positions), _ptr(head_out),
                              _stream(stream)))
 
@@ -345,10 +348,10 @@ def hts_paged_attn_workspace(B: int, q_heads: int, kv: hts_kv_desc, width: int, 
 def hts_paged_attn(q_heads: int, kv: hts_kv_desc, Q, k_cache, v_cache, block_table, lengths, scale: float, O,
                    k_scale=None, v_scale=None, window: int = 0, lse=None, workspace=None, stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().hts_paged_attn(_dt(Q.dtype), Q.shape[0], q_heads, ctypes.byref(kv), _ptr(Q), Q.stride(0),
+    _check(lib().hts_paged_attn(_dt(Q.dtype), Q.shape[0], q_heads, ctypes.byref(kv), _ptr(Q), _ld(Q),
                                 _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-                                block_table.stride(0), block_table.shape[1], _ptr(lengths), scale, window, _ptr(O),
-                                O.stride(0), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+                                _ld(block_table), block_table.shape[1], _ptr(lengths), scale, window, _ptr(O),
+                                _ld(O), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 def hts_residual_norm(desc: hts_norm_desc, M: int, N: int, block, post_weight, post_bias, gate, R, pre_weight,
