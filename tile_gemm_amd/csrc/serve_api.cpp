@@ -469,7 +469,6 @@ hts_status hts_paged_attn(int32_t dtype, int64_t B, int32_t q_heads, const hts_k
     a.v_scale = v_scale;
     a.table = block_table;
     a.ldt = ldt;
-    a.width = width;
     a.lengths = lengths;
     a.scale = scale;
     a.O = static_cast<uint16_t*>(O);

@@ -5,10 +5,6 @@
 
 namespace hts {
 
-template <typename T> __device__ __forceinline__ uint32_t narrow(float f) {
-    return T::id == BF16T::id ? narrow_bf16(f) : narrow_f16(f);
-}
-
 template <typename T> __device__ __forceinline__ void widen8(u32x4 v, float* f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

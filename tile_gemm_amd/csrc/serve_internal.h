@@ -64,7 +64,7 @@ struct AttnArgs {
     const void *kc, *vc;
     const float *k_scale, *v_scale;
     const int32_t* table;
-    int64_t ldt, width;
+    int64_t ldt;
     const int32_t* lengths;
     float scale;
     uint32_t window;           // 0: none
