@@ -149,6 +149,57 @@ def test_generation_matches_the_model_in_64_bits(cache_dtype, post):
         assert err.max() <= 24 * 2.0 ** -9 + (4 * 0.5 * 2.0 ** -4 / 3 ** 0.5 if cache_dtype != torch.bfloat16 else 0.0)
 
 
+@pytest.mark.parametrize("cache_dtype", [torch.bfloat16, torch.float8_e4m3fn], ids=["bf16", "fp8"])
+def test_blocks_attend_to_what_their_cache_holds(cache_dtype):
+    # each block's cache and output product in its own step, so that a scale or a window that is wrong in one of them
+    # shows: the cache against k and v in 64 bits, the product against 64-bit attention over that cache
+    model = Model(cache_dtype, seed=12, post=False)
+    B, steps = 3, 40
+    g = torch.Generator(device=DEV)
+    g.manual_seed(13)
+    free, table = torch.randperm(64, generator=g, device=DEV).int(), torch.full((B, 8), -1, dtype=torch.int32, device=DEV)
+    cached, ones, head = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV), None
+    for t in range(steps):
+        x, r = torch.randn((B, HID), generator=g, device=DEV).bfloat16(), None
+        st = hts.kv_step(cached, ones, free, table, PAGE, B, free_head=head)
+        for n, (layer, w) in enumerate(zip(model.layers, model.dense)):
+            bufs = block.buffers(B, layer.weights, torch.bfloat16, DEV)
+            stream = x.double() if r is None else (r.float() + x.float()).double()
+            x, r = block.decode(x, r, layer, st, table, model.plan, bufs)
+            if t not in (0, steps - 1):
+                continue
+            c = layer.cache
+            ks, vs = ((1.0, 1.0) if c.k_scale is None else (s.double().cpu().numpy()[:, None] for s in (c.k_scale, c.v_scale)))
+            kc, vc = c.k.float().double().cpu().numpy() * ks, c.v.float().double().cpu().numpy() * vs
+            tab, weight = table.cpu().numpy(), layer.input_norm.weight.double()
+            y = (stream / torch.sqrt((stream ** 2).mean(1, keepdim=True) + 1e-5) * weight).cpu().numpy()
+            at = np.arange(max(0, t + 1 - layer.window) if layer.window else 0, t + 1)
+            for b in range(B):
+                k, v = y[b] @ w["k"].T, y[b] @ w["v"].T
+                k = ref.rope(k[None], np.array([t]), ref.rope_turns(64), DIM, "interleaved", 1.0)[0]
+                ids = tab[b, at // PAGE]
+                for want, held, s, m in ((k.reshape(HK, DIM), kc, ks, w["k"]), (v.reshape(HK, DIM), vc, vs, w["v"])):
+                    got = held[ids[-1], t % PAGE]
+                    # half steps of 2^-8: y's through the product (its largest gain), k or v after it, k turned; then the
+                    # cache's: the same, or 2^-4 of the value and 2^-10 among the small ones
+                    tol = 2.0 ** -8 * (np.linalg.norm(m, 2) * np.linalg.norm(y[b]) + 2 * np.linalg.norm(want))
+                    if cache_dtype != torch.bfloat16:
+                        tol += 2.0 ** -4 * np.linalg.norm(want) + 2.0 ** -10 * np.max(s) * want.size ** 0.5
+                    assert np.linalg.norm(got - want) <= tol, (n, t, b)
+                q = bufs["q"][b].double().cpu().numpy().reshape(HQ, DIM)
+                a = np.zeros((HQ, DIM))
+                for h in range(HQ):
+                    sc = kc[ids, at % PAGE, h // 2] @ q[h] * DIM ** -0.5
+                    p = np.exp(sc - sc.max())
+                    a[h] = p @ vc[ids, at % PAGE, h // 2] / p.sum()
+                want, got = w["o"] @ a.reshape(-1), bufs["o"][b].double().cpu().numpy()
+                # attention rounded once (through the product's largest gain), the product once, and 32-bit sums
+                tol = 2.0 ** -8 * (np.linalg.norm(w["o"], 2) * np.linalg.norm(a) + np.linalg.norm(want)) * (1 + 2.0 ** -6)
+                say(f"[decode] {cache_dtype} layer {n} step {t} request {b}: {np.linalg.norm(got - want):.2e} of {tol:.2e}")
+                assert np.linalg.norm(got - want) <= tol
+        cached, head = st.lengths, st.head
+
+
 def test_generation_on_row_major_weights():
     # the same blocks on the unpacked weights: the same products up to the order of their sums
     model = Model(torch.bfloat16, seed=4)
