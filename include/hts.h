@@ -313,8 +313,8 @@ typedef struct {
  *   slots     : int64[tokens]   page id * page + place in the page, or -1 (no page, or the position
  *                               lies past the table's width)
  *   positions : int32[tokens]   the token's position in its request
- *   head_out  : int32[1]        *free_head plus the pages the step opens (above n_free when the
- *                               list was too short)
+ *   head_out  : int32[1]        *free_head (negative: 0) plus the pages the step opens (above n_free when
+ *                               the list was too short)
  * Tokens past the step's last one, up to `tokens`, get slot and position -1: a step captured for
  * `tokens` tokens runs any smaller batch.  Tokens past `tokens` are not written.  Sums past
  * 2^31 - 1 saturate.  0 <= B <= 4096; width, ldt, n_free, tokens and B * width below 2^31; outputs must not
@@ -365,7 +365,8 @@ typedef struct {
  * [T, k_heads*dim], each row by its position (device int32[T]; int32 covers any context).  The
  * angle is reduced to one turn in 64 bits, the rotation is 32-bit, rounded once.  A row whose
  * position is negative is not written.  Q_out may be Q and K_out may be K (same leading
- * dimension); q_heads or k_heads may be 0 (its pointers are not used).  turns: device
+ * dimension), with no other overlap between what is read and what is written; q_heads or k_heads may be
+ * 0 (its pointers are not used).  turns: device
  * double[rot/2] from hts_rope_plan, 8-byte aligned.  Matrices 16-byte aligned, leading dimensions
  * multiples of 8. */
 hts_status hts_rope(const hts_rope_desc* d, const double* turns, int64_t T, const int32_t* positions,
@@ -405,12 +406,12 @@ hts_status hts_rope_cache_rows(const hts_rope_desc* d, const double* turns, int6
  * accumulators are 32-bit.  Weights are held to 2^-24 of their value for HTS_BF16, and for HTS_F16 to
  * 2^-21, or 2^-43 of the largest weight where that is more.  O is rounded once to dtype.  A request
  * with no token (or only scores of minus infinity) gets zeros.  An infinity in the V of a token that
- * counts gives NaN or infinity in its entry.  lse (float [B, q_heads], or NULL) receives m + ln sum e^(s_t - m),
- * minus infinity for such a request: two calls over parts of a context can be joined by it.
+ * counts gives NaN or infinity in its entry.  lse (float [B, q_heads], or NULL) receives
+ * m + ln sum e^(s_t - m), minus infinity for such a request: two calls over parts of a context can be joined by it.
  * What the cache holds past a request's tokens is never used (NaN there does no harm).
  * Q, O: [B, q_heads*dim] in dtype (HTS_F16 / HTS_BF16), 16-byte aligned, leading dimensions
- * multiples of 8; O may be Q.  The cache has dtype or HTS_FP8_E4M3.  q_heads is a multiple of
- * kv->heads.  B <= 65535.  block_table: device int32 [B, ldt], `width` columns used.
+ * multiples of 8; O may be Q, and nothing else that is written may overlap what is read.  The cache has
+ * dtype or HTS_FP8_E4M3.  q_heads is a multiple of kv->heads.  B <= 65535.  block_table: device int32 [B, ldt], `width` columns used.
  * workspace: hts_paged_attn_workspace() bytes (16-byte aligned); the length is then split over
  * workgroups and joined by a second kernel in a fixed order.  With less, or NULL, each request and
  * head runs unsplit.  Results are deterministic for given lengths, shape and workspace size.

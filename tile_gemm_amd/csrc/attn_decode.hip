@@ -1,8 +1,8 @@
 // Attention of one new token per request over a paged key-value cache (hts_paged_attn).
 //
 // s_t = scale q.k_t, O = sum_t 2^(s_t log2e - m) v_t / sum_t 2^(s_t log2e - m): one pass over the
-// tokens with a running maximum m, sum l and accumulator.  Bound by HBM: K and V are read once, and
-// a new token brings only 4 operations per cached value and query head.
+// tokens with a running maximum m, sum l and accumulator.  Bound by HBM: K and V are read once per 16
+// query heads of a cache head, and a new token brings only 4 operations per cached value and query head.
 //
 // A workgroup (4 waves) takes one request, one cache head, up to 16 of the query heads that share
 // it, and a range of tokens; each wave takes every fourth step of 32 tokens (or 16, with halves of the
@@ -641,7 +641,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
 
 // Tokens of a step.  16 leave room for more waves, or for heads above 128 entries without spills (16 requests up to
 // 8192, 16/4 heads of 256: 57.7 us against 71.1; 32/8 heads of 64: 34.5 against 35.9; 64 up to 8191 on an 8-bit cache:
-// 102.5 against 104.3); 32 keep more of a long 16-bit cache of 128-entry heads in flight per wave (4 requests up to
+// 102.5 against 104.3; there of 64: 143 up to 1500, 10/10 heads 47.7 against 49.4, 64 up to 4096, 32/8 36.8 against 38.2);
+// 32 keep more of a long 16-bit cache of 128-entry heads in flight per wave (4 requests up to
 // 131072: 236.8 against 241.7, 32 up to 4096: 58.4 against 59.8), and halve the steps of a request that is not cut.
 template <bool C8, int DP, bool FULL, bool SPLIT>
 constexpr int kTok = DP == 256 || (SPLIT && !(DP == 128 && FULL && !C8)) ? 16 : 32;

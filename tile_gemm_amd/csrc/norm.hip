@@ -7,9 +7,9 @@
 // a wave (no barrier, 16 or 8 rows per workgroup); longer ones a workgroup each.
 // Bound by HBM: block, R and a per-token gate in, R' and Y out, once each.  The outputs are written past the
 // caches' normal lines (non-temporal): another XCD will read them, and the inputs keep their place (1000 x
-// 16384: 24.4 us against 32 with ordinary stores).  16384 x 4096, layer norms on both sides and a sigmoid gate:
-// 126-135 us, 5.0-5.3 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 2.6 us.  Sums go by row moves within a wave and one
-// barrier each (10 x 6568, two layer norms: 6.1 us against 7.5 with shuffles through LDS and two barriers).
+// 16384: 21.1 us against 30.4 with ordinary stores).  16384 x 4096, layer norms on both sides and a sigmoid gate:
+// 126 us, 5.3 TB/s (a copy of 4 GB reaches 4.8); 1 x 4096: 3.0 us.  Sums go by row moves within a wave and one
+// barrier each (10 x 6568, two layer norms: a fifth less time than with shuffles through LDS and two barriers).
 #include "serve_device.h"
 #include "serve_internal.h"
 
@@ -173,10 +173,12 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
     };
     const auto threads = [&](int ch) { return dim3((unsigned)(((chunks + ch - 1) / ch + 63) / 64 * 64)); };
     const dim3 grid = rows_of(1);
-    // Lanes of a wave for short rows (65536 x 128: 11.6 us against 22.1 with a workgroup of one wave each, 65536 x 256:
-    // 21.6 against 23.0).  Else one chunk per thread while the rows are few, for the shortest chain (1 x 4096:
-    // 2.8 us against 3.5 with two; 2048 x 4096: 12.1 against 12.6), two for many (16384 x 4096 with gate and layer
-    // norms: 138 against 152), four past 8192 entries (1000 x 16384: 21.3 against 24.4 with two).
+    // Lanes of a wave for short rows (65536 x 128: 11.8 us against 20.9 with a workgroup of one wave each, 65536 x 256:
+    // 21.9 against 22.6).  Else one chunk per thread while the rows are few, for the shortest chain (1 x 4096:
+    // 3.5 us against 3.8 with two; 2048 x 4096: 12.1 against 12.4), two for many (16384 x 4096 with gate and layer
+    // norms: 144 against 160 with one), four past 8192 entries (1000 x 16384, two layer norms: 25.8 against 26.3 with
+    // two; one RMS norm 21.1 and 20.8), but two in a small batch (10 x 15328: 6.8 against 7.2 with four; 64 x 16384: 7.1
+    // and 7.7).  Replays of a graph, whose kernels follow one another: a large one takes longer there than by itself.
     const bool few = a.M <= 2048;
     if (chunks <= 16) residual_norm_kernel<T, R32, 16, 1><<<rows_of(16), 256, 0, s>>>(a);
     else if (chunks <= 32) residual_norm_kernel<T, R32, 32, 1><<<rows_of(8), 256, 0, s>>>(a);

@@ -115,8 +115,9 @@ AttnPlan attn_plan(int64_t B, int32_t q_heads, const hts_kv_desc* kv, int64_t wi
     // 256 CUs hold three or four workgroups each, two of those for heads above 128 entries.  Four pay for smaller heads
     // of 16 bits (16 requests up to 4096, 16/4 heads of 96: 17.0 us with 1024 runs, 18.3 with 768; 64 requests up to 8191
     // on an 8-bit cache: 113.9 and 112.4).  Fewer stream as fast where each has long stretches to itself, and leave
-    // fewer parts: one a CU for heads above 128 (16 requests up to 8192, 16/4 heads of 256: 57.7 us with 256 runs, 59.4
-    // with 512), two where a page holds a head's tokens one after another (256 requests up to 2048, 32/8 heads, pages
+    // fewer parts: one a CU for heads above 128 (16 requests up to 8192, 16/4 heads of 256: 58.2 us with 256 runs, 59.7
+    // with 512; of 192 46.5 and 48.1; on an 8-bit cache 37.1 and 37.3, of 192 33.5 and 32.9; 30 up to 1142 there, 5/5 of
+    // 192: 22.1 and 26.2; 64 up to 2048, 8/8 of 160: 71.3 and 70.7), two where a page holds a head's tokens one after another (256 requests up to 2048, 32/8 heads, pages
     // of 64: 200 us with 512, 206 with 768; with the heads of a token together, 221 and 209), as it does where there is one
     // head, whose stride is not used (64 up to 8191, 16/1 heads: 36.1 us with 512, 40.1 with 768; 4 up to 131072, 8/1: 39.9
     // and 42.0; 32 up to 4096, 4/1: 14.8 and 14.7).

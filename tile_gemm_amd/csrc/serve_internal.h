@@ -83,8 +83,10 @@ struct AttnArgs {
 };
 // Requests whose runs every wave finds by one scan; more run unsplit.
 constexpr int64_t kMaxSplitRequests = 4096;
-// Where no request can be longer, each is one workgroup's (51 requests up to 455 tokens, 21/3 heads of 192: 17 us
-// against 32 in runs with a join).
+// Where no request can be longer, each is one workgroup's (51 requests up to 455 tokens, 21/3 heads of 192: 12.5 us
+// against 21.5 in runs with a join; 4 up to 512, 8/2 of 128: 7.9 and 9.2; 64 up to 512, 32/8: 16.6 and 21.1).  Up to
+// 1000 tokens a small batch is faster in runs (4 requests, 8/2 of 128: 9.5 against 12.4), a large one slower (51, 21/3
+// of 192: 24.5 against 20.2).
 constexpr int kAttnWholeTokens = 512;
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
