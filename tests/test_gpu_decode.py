@@ -324,3 +324,16 @@ def test_block_refuses_shapes_that_do_not_fit():
     for bad in (x.half(), x[:1], x[:, :256]):
         with pytest.raises(hts.HTSError):
             block.decode(bad, None, layer, st, table, model.plan)
+
+
+def test_block_refuses_before_it_writes_to_the_cache():
+    # what only attention would refuse, behind the cache write of the same step
+    model = Model(torch.bfloat16, seed=6)
+    layer = model.layers[0]
+    args = layer.cache, layer.input_norm, layer.mlp_norm
+    q, o = (torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in ((3 * DIM, HID), (HID, 3 * DIM)))
+    for change, kw in ((dict(q=q, o=o), {}), ({}, dict(window=-1)), ({}, dict(attn_scale=float("nan"))),
+                       ({}, dict(attn_scale=float("inf")))):
+        with pytest.raises(hts.HTSError):
+            block.Layer({**layer.weights, **change}, *args, **kw)
+    block.Layer({**layer.weights, "q": q[:2 * DIM], "o": o[:, :2 * DIM].contiguous()}, *args, window=5, attn_scale=0.1)

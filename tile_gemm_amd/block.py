@@ -28,6 +28,7 @@ one ``kv_step`` for all layers, then ``decode`` per layer:
 from __future__ import annotations
 
 import dataclasses
+import math
 from typing import Dict, Optional
 
 import torch
@@ -116,6 +117,13 @@ class Layer:
                 raise HTSError(2, f"{n} has type {t}: a block's weights share one 16-bit type")
             if got != want[n]:
                 raise HTSError(3, f"{n} is {got[0]} x {got[1]}, the block's other shapes ask for {want[n][0]} x {want[n][1]}")
+        # what attention would refuse after the step's keys and values are in the cache
+        if nq % nk:
+            raise HTSError(3, f"q has {nq} rows, not a multiple of the cache's {self.cache.heads} heads of {self.cache.dim}")
+        if self.window < 0:
+            raise HTSError(3, f"window={self.window} is negative")
+        if self.attn_scale is not None and not math.isfinite(self.attn_scale):
+            raise HTSError(1, "attn_scale is not finite")
 
 
 def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step: KVStep, block_table: torch.Tensor,
