@@ -459,6 +459,85 @@ hts_status hts_residual_norm(const hts_norm_desc* d, int64_t M, int64_t N, const
                              const void* R, int64_t ldr, const void* pre_weight, const void* pre_bias,
                              void* R_out, int64_t ldro, void* Y, int64_t ldy, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 8-bit linear layers with a scale for each block of 128.  hts_gemm and hts_dense_gemm take E4M3 values as they
+ * are; a model in 8 bits stores value / scale, with a float scale for each row of the activations and 128 columns,
+ * and for each 128 x 128 block of a weight.  These entry points make such values, multiply them, and run a decoder
+ * block's feed-forward part on them.  Weights are row-major, as a checkpoint holds them, and dense.  The conventions
+ * above hold; nothing here has a backward pass, as in the rest of the library.
+ *
+ * Blocks start at multiples of 128; the last one of a row or column may be shorter.  With KB = ceil(K / 128):
+ *   rows    : values E4M3 [M, K], leading dimension a multiple of 16; scale float [KB, lds], lds >= M: the scale of
+ *             row m and block b at b*lds + m
+ *   weights : values E4M3 [N, K], leading dimension a multiple of 16; scale float [ceil(N / 128), lds], lds >= KB:
+ *             the scale of rows 128 r .. 128 r + 127 and block b at r*lds + b
+ * Values are 16-byte aligned, scales 4-byte.  K is a multiple of 16 (a 16-byte chunk of a row), and leading
+ * dimensions of values are below 2^22.  M and N are below 2^26, and M * N below 2^36.
+ * ------------------------------------------------------------------------------------------ */
+
+/* A weight (a host structure; values and scale are device memory). */
+typedef struct {
+    const void* values;
+    int64_t ld;
+    const float* scale;
+    int64_t ld_scale;
+} hts_scaled_weight;
+
+/* Device, asynchronous.  X[M,K] (HTS_F16, HTS_BF16 or HTS_F32, 16-byte aligned, ldx a multiple of 8) to E4M3 values
+ * with a scale for each row and block:
+ *     a = max(largest magnitude of the block, 2^-100),  scale = a / 448,  value = E4M3(x * (448 / a))
+ * Each quotient and product is rounded once to 32 bits, the value to nearest even.  A NaN counts for nothing in a
+ * and stays NaN; an infinity makes its block's scale infinite, its finite values 0 and itself NaN.  Q must not overlap X.
+ * M == 0 is a no-op. */
+hts_status hts_quantize_rows(int32_t dtype, int64_t M, int64_t K, const void* X, int64_t ldx, void* Q, int64_t ldq,
+                             float* scale, int64_t lds, void* stream);
+
+/* Device, asynchronous.  The same for a weight W[N,K], with one scale for each 128 x 128 block. */
+hts_status hts_quantize_weight(int32_t dtype, int64_t N, int64_t K, const void* W, int64_t ldw, void* Q, int64_t ldq,
+                               float* scale, int64_t lds, void* stream);
+
+/* Device, asynchronous.  The block-scaled product
+ *     Y[m,n] = sum_b x_scale[b,m] * w_scale[n/128,b] * sum_{k in b} X[m,k] * W[n,k]
+ * Y as HTS_F32, HTS_F16 or HTS_BF16, ldy >= N a multiple of 4, 16-byte aligned, any N.  Each block's sum is made by
+ * one 8-bit matrix instruction, which keeps, in every group of eight products, 13 bits below the largest one's
+ * power of two; the scaled sums are added in 32 bits and rounded once.  For values spread as a quantised normal
+ * distribution that is an error of 1.5e-5 in the 2-norm, also of an HTS_F32 output.  The product of the two scales
+ * is 32-bit too.  A NaN value, or a NaN or infinite scale, makes its row or column of Y NaN or infinite.
+ * Rows past M are not read.  M == 0 is a no-op.  workspace: hts_scaled_gemm_workspace() bytes, 16-byte aligned, or NULL:
+ * with less the product runs unsplit, with another order of its 32-bit sums.  Results are deterministic for a given
+ * shape and workspace.  Calls that share a workspace must not overlap. */
+hts_status hts_scaled_gemm(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* x_scale,
+                           int64_t ldxs, const hts_scaled_weight* W, void* Y, int64_t ldy, int32_t y_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+hts_status hts_scaled_gemm_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes);
+
+/* What the gate goes through: x / (1 + e^-x); x P(Z <= x) of a standard normal Z; the same with P by its tanh form. */
+enum { HTS_ACT_SILU = 0, HTS_ACT_GELU = 1, HTS_ACT_GELU_TANH = 2 };
+
+/* Device, asynchronous.  H = act(X . gate^T) * (X . up^T), gate and up [N,K], both products and the step between them
+ * in one kernel (split products: and one for the sum of their parts), 32-bit until H is rounded once.
+ *   h_dtype HTS_F32, HTS_F16, HTS_BF16 : h_scale must be NULL; ldh >= N a multiple of 4, any N
+ *   h_dtype HTS_FP8_E4M3               : H rows of values and h_scale [ceil(N/128), ldhs] as hts_quantize_rows makes
+ *                                        them of the unrounded H; N and ldh multiples of 16.  The next product's X.
+ * workspace: hts_scaled_gated_workspace() bytes; optional except where h_dtype is HTS_FP8_E4M3 and M is at most 32
+ * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm. */
+hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                            const float* x_scale, int64_t ldxs, const hts_scaled_weight* gate,
+                            const hts_scaled_weight* up, void* H, int64_t ldh, int32_t h_dtype, float* h_scale,
+                            int64_t ldhs, void* workspace, size_t workspace_bytes, void* stream);
+hts_status hts_scaled_gated_workspace(int64_t M, int64_t N, int64_t K, int32_t h_dtype, size_t* bytes);
+
+/* Device, asynchronous.  A decoder block's feed-forward part on 8-bit weights:
+ *     Y = q(act(q(X) . gate^T) * (q(X) . up^T)) . down^T,   q = hts_quantize_rows
+ * X [M, hidden] and Y [M, hidden] in dtype (HTS_F16 or HTS_BF16), 16-byte aligned, leading dimensions multiples of 8; gate
+ * and up [inner, hidden], down [hidden, inner]; hidden and inner multiples of 16.  Y may be X (with the same leading
+ * dimension).  workspace: hts_scaled_mlp_workspace() bytes, 16-byte aligned, required where M > 0. */
+hts_status hts_scaled_mlp(int32_t act, int32_t dtype, int64_t M, int64_t hidden, int64_t inner, const void* X,
+                          int64_t ldx, const hts_scaled_weight* gate, const hts_scaled_weight* up,
+                          const hts_scaled_weight* down, void* Y, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream);
+hts_status hts_scaled_mlp_workspace(int64_t M, int64_t hidden, int64_t inner, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

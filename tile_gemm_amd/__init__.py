@@ -10,7 +10,8 @@ Low-level functions carry the C names (``hts_pack_plan``, ``hts_pack``,
 ``unpack``, ``dense_gemm``, ``pack_masked``, ``wanda_tile_map`` and
 ``wanda_global_maps`` are tensor-level helpers built on them.  The steps of a decoder block around its
 products (``kv_step``, ``rope``, ``rope_cache``, ``paged_attn``, ``residual_norm``) have theirs in
-``serving``, under this package's name too.
+``serving``, the block-scaled 8-bit layers (``ScaledWeight``, ``quantize_rows``, ``scaled_gemm``, ``scaled_gated``,
+``scaled_mlp``) in ``scaled``; both under this package's name too.
 """
 from __future__ import annotations
 
@@ -72,6 +73,13 @@ class hts_norm_desc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("gate_act", ctypes.c_int32)]
 
 
+class hts_scaled_weight(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("ld_scale", ctypes.c_int64)]
+
+
+HTS_ACT_SILU, HTS_ACT_GELU, HTS_ACT_GELU_TANH = 0, 1, 2
+
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -114,6 +122,19 @@ _SIGS = {
                                                 ctypes.POINTER(ctypes.c_size_t)]),
     "hts_residual_norm": (ctypes.c_int, [ctypes.POINTER(hts_norm_desc), _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I64,
                                          _VP, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP]),
+    "hts_quantize_rows": (ctypes.c_int, [_I32, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "hts_quantize_weight": (ctypes.c_int, [_I32, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "hts_scaled_gemm": (ctypes.c_int, [_I64, _I64, _I64, _VP, _I64, _VP, _I64, ctypes.POINTER(hts_scaled_weight), _VP,
+                                       _I64, _I32, _VP, ctypes.c_size_t, _VP]),
+    "hts_scaled_gemm_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "hts_scaled_gated": (ctypes.c_int, [_I32, _I64, _I64, _I64, _VP, _I64, _VP, _I64, ctypes.POINTER(hts_scaled_weight),
+                                        ctypes.POINTER(hts_scaled_weight), _VP, _I64, _I32, _VP, _I64, _VP,
+                                        ctypes.c_size_t, _VP]),
+    "hts_scaled_gated_workspace": (ctypes.c_int, [_I64, _I64, _I64, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    "hts_scaled_mlp": (ctypes.c_int, [_I32, _I32, _I64, _I64, _I64, _VP, _I64, ctypes.POINTER(hts_scaled_weight),
+                                      ctypes.POINTER(hts_scaled_weight), ctypes.POINTER(hts_scaled_weight), _VP, _I64, _VP,
+                                      ctypes.c_size_t, _VP]),
+    "hts_scaled_mlp_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -361,6 +382,77 @@ def hts_residual_norm(desc: hts_norm_desc, M: int, N: int, block, post_weight, p
                                    _ptr(pre_bias), _ptr(R_out), _ld(R_out), _ptr(Y), _ld(Y), _stream(stream)))
 
 
+def hts_quantize_rows(X, Q, scale, stream=None) -> None:
+    """scale: the [blocks, rows] matrix of the C call."""
+    M, K = X.shape
+    _check(lib().hts_quantize_rows(_dt(X.dtype), M, K, _ptr(X), _ld(X), _ptr(Q), _ld16(Q), _ptr(scale), _lds(scale),
+                                   _stream(stream)))
+
+
+def hts_quantize_weight(W, Q, scale, stream=None) -> None:
+    N, K = W.shape
+    _check(lib().hts_quantize_weight(_dt(W.dtype), N, K, _ptr(W), _ld(W), _ptr(Q), _ld16(Q), _ptr(scale), _lds(scale),
+                                     _stream(stream)))
+
+
+def _ld16(t: Optional[torch.Tensor]) -> int:
+    """Leading dimension of E4M3 rows (one row: any that the library takes)."""
+    if t is None or t.dim() != 2:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _lds(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _weight(w: Optional[hts_scaled_weight]):
+    return None if w is None else ctypes.byref(w)
+
+
+def hts_scaled_gemm_workspace(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hts_scaled_gemm_workspace(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def hts_scaled_gemm(X, x_scale, W: hts_scaled_weight, Y, workspace=None, stream=None) -> None:
+    """x_scale: the [blocks, rows] matrix of the C call."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().hts_scaled_gemm(X.shape[0], Y.shape[1], X.shape[1], _ptr(X), _ld16(X), _ptr(x_scale), _lds(x_scale),
+                                 _weight(W), _ptr(Y), _ld16(Y), _dt(Y.dtype), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def hts_scaled_gated_workspace(M: int, N: int, K: int, h_dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hts_scaled_gated_workspace(M, N, K, _dt(h_dtype), ctypes.byref(n)))
+    return n.value
+
+
+def hts_scaled_gated(act: int, X, x_scale, gate: hts_scaled_weight, up: hts_scaled_weight, H, h_scale=None,
+                     workspace=None, stream=None) -> None:
+    """x_scale, h_scale: the [blocks, rows] matrices of the C call."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().hts_scaled_gated(act, X.shape[0], H.shape[1], X.shape[1], _ptr(X), _ld16(X), _ptr(x_scale),
+                                  _lds(x_scale), _weight(gate), _weight(up), _ptr(H), _ld16(H), _dt(H.dtype),
+                                  _ptr(h_scale), 0 if h_scale is None else _lds(h_scale), _ptr(workspace), ws_bytes,
+                                  _stream(stream)))
+
+
+def hts_scaled_mlp_workspace(M: int, hidden: int, inner: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hts_scaled_mlp_workspace(M, hidden, inner, ctypes.byref(n)))
+    return n.value
+
+
+def hts_scaled_mlp(act: int, inner: int, X, gate: hts_scaled_weight, up: hts_scaled_weight, down: hts_scaled_weight, Y,
+                   workspace=None, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().hts_scaled_mlp(act, _dt(X.dtype), X.shape[0], X.shape[1], inner, _ptr(X), _ld(X), _weight(gate),
+                                _weight(up), _weight(down), _ptr(Y), _ld(Y), _ptr(workspace), ws_bytes,
+                                _stream(stream)))
+
+
 # --------------------------------------------------------------------------
 # tensor-level helpers
 # --------------------------------------------------------------------------
@@ -561,3 +653,4 @@ def bits_from_tensor(t: torch.Tensor) -> np.ndarray:
 
 from .serving import (KVCache, KVStep, Norm, RopePlan, kv_cache, kv_step, paged_attn, residual_norm, rope,  # noqa: E402
                       rope_cache, rope_plan)
+from .scaled import ScaledWeight, quantize_rows, scaled_gated, scaled_gemm, scaled_mlp  # noqa: E402

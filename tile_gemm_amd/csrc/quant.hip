@@ -1,0 +1,121 @@
+// Rows and weights to E4M3 values with a 32-bit scale for each block of 128.
+//
+//   a = max(max |x|, 2^-100) over the block,   s = a / 448,   q = E4M3(x * (448 / a))
+//
+// Each quotient and product is one 32-bit operation, rounded to nearest; E4M3 rounds to nearest even and x * (448 / a)
+// stays within 448 up to its last bit.  NaN counts for nothing in a and stays NaN; an infinity makes s infinite and the
+// block's finite values 0.
+#include "scaled_device.h"
+
+namespace hts {
+namespace {
+
+// 16 consecutive values at column c of a row (c and K multiples of 16), as floats.
+template <int DT>
+__device__ __forceinline__ void load16(const void* row, int64_t c, float (&f)[16]) {
+    if constexpr (DT == HTS_F32) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 v = p[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * i + e] = v[e];
+        }
+    } else {
+        using T = typename std::conditional<DT == HTS_BF16, BF16T, F16T>::type;
+        const uint16_t* p = static_cast<const uint16_t*>(row) + c;
+        widen8<T>(ld16(p), f);
+        widen8<T>(ld16(p + 8), f + 8);
+    }
+}
+
+__device__ __forceinline__ float top16(const float (&f)[16]) {
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) t = fmaxf(t, fabsf(f[e]));
+    return t;
+}
+
+__device__ __forceinline__ u32x4 scaled16(float (&f)[16], float r) {
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] *= r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = narrow4_e4m3(f + 4 * i);
+    return q;
+}
+
+// Eight lanes to a block of a row, 16 values each; a workgroup's 32 blocks run along the row.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a, int64_t KB) {
+    const int64_t id = (blockIdx.y * kGridX + blockIdx.x) * 32 + (threadIdx.x >> 3);
+    const int64_t m = id / KB, kb = id % KB;
+    if (m >= a.M) return;
+    const int64_t c = kb * kScaleBlock + 16 * (threadIdx.x & 7);
+    const bool in = c < a.K;
+    float f[16] = {};
+    constexpr int ES = DT == HTS_F32 ? 4 : 2;
+    if (in) load16<DT>(static_cast<const uint8_t*>(a.X) + m * a.ldx * ES, c, f);
+    float t = top16(f);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
+    t = fmaxf(t, kLeastTop);
+    if (in) st16(a.Q + m * a.ldq + c, scaled16(f, kE4m3Max / t));
+    if ((threadIdx.x & 7) == 0) a.S[kb * a.lds + m] = t / kE4m3Max;
+}
+
+// A workgroup to a 128 x 128 block: eight lanes to a row, 32 rows at a time.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_weight_kernel(const QuantArgs a, int64_t KB) {
+    __shared__ float wave_top[4];
+    const int64_t id = blockIdx.y * kGridX + blockIdx.x;
+    const int64_t nb = id / KB, kb = id % KB;
+    if (nb * kScaleBlock >= a.M) return;
+    const int64_t c = kb * kScaleBlock + 16 * (threadIdx.x & 7);
+    const int64_t row0 = nb * kScaleBlock + (threadIdx.x >> 3);
+    constexpr int ES = DT == HTS_F32 ? 4 : 2;
+    float f[4][16] = {};
+    float t = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int64_t n = row0 + 32 * v;
+        if (n < a.M && c < a.K) load16<DT>(static_cast<const uint8_t*>(a.X) + n * a.ldx * ES, c, f[v]);
+        t = fmaxf(t, top16(f[v]));
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
+    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = t;
+    __syncthreads();
+    t = fmaxf(fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3])), kLeastTop);
+    const float r = kE4m3Max / t;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const int64_t n = row0 + 32 * v;
+        if (n < a.M && c < a.K) st16(a.Q + n * a.ldq + c, scaled16(f[v], r));
+    }
+    if (threadIdx.x == 0) a.S[nb * a.lds + kb] = t / kE4m3Max;
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s) {
+    const int64_t KB = scale_blocks(a.K);
+    const WideGrid wide = wide_grid((a.M * KB + 31) / 32);
+    const dim3 grid(wide.x, wide.rest), block(256);
+    if (a.dtype == HTS_F32) quantize_rows_kernel<HTS_F32><<<grid, block, 0, s>>>(a, KB);
+    else if (a.dtype == HTS_BF16) quantize_rows_kernel<HTS_BF16><<<grid, block, 0, s>>>(a, KB);
+    else quantize_rows_kernel<HTS_F16><<<grid, block, 0, s>>>(a, KB);
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize_weight(const QuantArgs& a, hipStream_t s) {
+    const int64_t KB = scale_blocks(a.K);
+    const WideGrid wide = wide_grid(scale_blocks(a.M) * KB);
+    const dim3 grid(wide.x, wide.rest), block(256);
+    if (a.dtype == HTS_F32) quantize_weight_kernel<HTS_F32><<<grid, block, 0, s>>>(a, KB);
+    else if (a.dtype == HTS_BF16) quantize_weight_kernel<HTS_BF16><<<grid, block, 0, s>>>(a, KB);
+    else quantize_weight_kernel<HTS_F16><<<grid, block, 0, s>>>(a, KB);
+    return hipGetLastError();
+}
+
+}  // namespace hts

@@ -1,0 +1,40 @@
+// Device pieces of the block-scaled 8-bit kernels.
+#pragma once
+
+#include "gemm_common.h"
+#include "scaled_internal.h"
+#include "serve_device.h"
+
+namespace hts {
+
+// A block's largest magnitude a (a zero block: 2^-100, so that its scale stays a normal number) gives its scale a / 448
+// and the factor 448 / a that its values are multiplied by; each is rounded once to 32 bits.
+constexpr float kLeastTop = 0x1p-100f, kE4m3Max = 448.0f;
+
+__device__ __forceinline__ float act_value(int act, float g) {
+    if (act == HTS_ACT_SILU) return g / (1.0f + expf(-g));
+    if (act == HTS_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678f));
+    // tanh form: g * sigmoid(2 z), z = sqrt(2 / pi) (g + 0.044715 g^3)
+    const float z = 1.5957691f * (g + 0.044715f * g * g * g);
+    return g / (1.0f + expf(-z));
+}
+
+// 16x16x128 product of E4M3 values from zero: the block's own sum, before its scales.  Unit block scales (the form
+// without scale operands).  Within each group of eight products along K the instruction keeps 13 bits below the largest
+// one's power of two and drops the rest (measured); groups are added in 32 bits.
+__device__ __forceinline__ f32x4 mfma_block(u32x8 a, u32x8 b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b),
+                                                            f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Up to four consecutive outputs of a row from column n on, those below N.
+__device__ __forceinline__ void store_upto4(void* Y, int64_t off, int64_t left, int32_t dt, f32x4 v) {
+    if (left >= 4) {
+        store_y4(Y, off, dt, v);
+    } else {
+        for (int e = 0; e < 3; ++e)
+            if (e < left) store_y1(Y, off + e, dt, v[e]);
+    }
+}
+
+}  // namespace hts

@@ -1,0 +1,63 @@
+// Internal declarations shared by the block-scaled 8-bit half of the C API and its gfx950 kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "hts.h"
+#include "serve_internal.h"
+
+namespace hts {
+
+constexpr int kScaleBlock = 128;
+inline int64_t scale_blocks(int64_t n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+
+// Rows to E4M3.  rows 1: a scale for each row and block at S[block * lds + row]; rows 128: one for each 128 x 128 block
+// at S[row / 128 * lds + block].
+struct QuantArgs {
+    int32_t dtype;
+    int64_t M, K;
+    const void* X;
+    int64_t ldx;
+    uint8_t* Q;
+    int64_t ldq;
+    float* S;
+    int64_t lds;
+};
+hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s);
+hipError_t launch_quantize_weight(const QuantArgs& a, hipStream_t s);
+
+// One block-scaled product, or the gated pair of them.
+struct ScaledArgs {
+    int64_t M, N, K;
+    const uint8_t* X;
+    int64_t ldx;
+    const float* xs;           // [blocks of K][ldxs], entry m
+    int64_t ldxs;
+    const uint8_t* W[2];       // the weight, or gate and up
+    int64_t ldw[2];
+    const float* ws[2];        // [blocks of N][ldws], entry = block of K
+    int64_t ldws[2];
+    int32_t act;               // HTS_ACT_* (gated)
+    int32_t gated;
+    void* Y;
+    int64_t ldy;
+    int32_t y_dtype;           // HTS_F32, HTS_F16, HTS_BF16, or HTS_FP8_E4M3 with ys (gated)
+    float* ys;                 // [blocks of N][ldys], entry m
+    int64_t ldys;
+    // nsplit > 1: the blocks of K are cut into nsplit parts; part p of weight w goes to part[(p * weights + w) * M * ldp]
+    float* part;
+    int64_t ldp;
+    int32_t nsplit;
+};
+
+// Rows of X up to which a product streams its weights past them.
+constexpr int64_t kScaledStreamRows = 32;
+hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s);
+// Tile shapes: rows of W and of X a workgroup.
+enum ScaledTile { TILE_256x256 = 0, TILE_256x128 = 1, TILE_128x128 = 2 };
+hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledTile shape, hipStream_t s);
+// The sum of a.nsplit parts, gated and rounded to Y.
+hipError_t launch_scaled_sum(const ScaledArgs& a, hipStream_t s);
+
+}  // namespace hts

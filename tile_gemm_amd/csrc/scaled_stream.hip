@@ -1,0 +1,192 @@
+// Block-scaled 8-bit product for few rows (M <= 32): the weights stream past the rows, and the sum of parts.
+//
+// A workgroup owns 16 outputs (the gated form: 16 gate rows and the same up rows) and KS waves; wave w takes the blocks
+// [KB w / KS, KB (w + 1) / KS) of K.  W and X go from global memory straight into the operands of the 16x16x128
+// instruction, NT blocks of loads ahead of their use; each block's sum is multiplied by both scales and added in 32 bits.
+// The waves' sums meet in LDS and are added in wave order.
+#include "scaled_device.h"
+
+namespace hts {
+namespace {
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kOutside = 0x80000000u;   // past every buffer's end (their bytes stay below 2^31): reads zeros
+
+__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+
+template <bool GATED, int KS, int NT, int MG>
+__global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs a) {
+    constexpr int PP = GATED ? 2 : 1;
+    __shared__ f32x4 red[KS][MG * PP * 64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int KB = (int)((a.K + 127) / 128);
+    const int kb0 = KB * wave / KS, kb1 = KB * (wave + 1) / KS;
+    const int rows = (int)(a.N - n0 < 16 ? a.N - n0 : 16);
+
+    rsrc_t wr[PP];
+    uint32_t wvo[PP];
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+        wr[p] = make_rsrc(a.W[p] + n0 * a.ldw[p], (uint32_t)((rows - 1) * a.ldw[p] + a.K));
+        wvo[p] = (uint32_t)((i < rows ? i : rows - 1) * a.ldw[p]) + 16 * g;
+    }
+    const rsrc_t xr = make_rsrc(a.X, (uint32_t)((a.M - 1) * a.ldx + a.K));
+    uint32_t xvo[MG];
+    const float* xs[MG];
+#pragma unroll
+    for (int h = 0; h < MG; ++h) {
+        const int m = 16 * h + i < (int)a.M ? 16 * h + i : (int)a.M - 1;
+        xvo[h] = (uint32_t)(m * a.ldx) + 16 * g;
+        xs[h] = a.xs + m;
+    }
+    const int tail = (int)(a.K - (int64_t)128 * (KB - 1));
+    const float* ws[PP];
+#pragma unroll
+    for (int p = 0; p < PP; ++p) ws[p] = a.ws[p] + n0 / 128 * a.ldws[p];
+
+    f32x4 acc[MG][PP];
+#pragma unroll
+    for (int h = 0; h < MG; ++h)
+#pragma unroll
+        for (int p = 0; p < PP; ++p) acc[h][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int t = kb0; t < kb1; t += NT) {
+        u32x4 W[NT][PP][2], X[NT][MG][2];
+        float sx[NT][MG], sw[NT][PP];
+#pragma unroll
+        for (int s = 0; s < NT; ++s) {
+            if (t + s >= kb1) break;
+            const int kb = t + s;
+            const bool cut = kb == KB - 1;
+            const uint32_t so = 128u * kb;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bool out = cut && 16 * (g + 4 * u) >= tail;
+#pragma unroll
+                for (int p = 0; p < PP; ++p) W[s][p][u] = load16(wr[p], out ? kOutside : wvo[p] + 64 * u, so);
+#pragma unroll
+                for (int h = 0; h < MG; ++h) X[s][h][u] = load16(xr, out ? kOutside : xvo[h] + 64 * u, so);
+            }
+#pragma unroll
+            for (int h = 0; h < MG; ++h) sx[s][h] = xs[h][kb * a.ldxs];
+#pragma unroll
+            for (int p = 0; p < PP; ++p) sw[s][p] = ws[p][kb];
+        }
+#pragma unroll
+        for (int s = 0; s < NT; ++s) {
+            if (t + s >= kb1) break;
+#pragma unroll
+            for (int h = 0; h < MG; ++h)
+#pragma unroll
+                for (int p = 0; p < PP; ++p) {
+                    const f32x4 v = mfma_block(cat8(W[s][p][0], W[s][p][1]), cat8(X[s][h][0], X[s][h][1]));
+                    const float sc = sx[s][h] * sw[s][p];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[h][p][e] = __builtin_fmaf(v[e], sc, acc[h][p][e]);
+                }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < MG; ++h)
+#pragma unroll
+        for (int p = 0; p < PP; ++p) red[wave][(h * PP + p) * 64 + lane] = acc[h][p];
+    __syncthreads();
+    // output (row m, column r of the 16): four columns of a row lie in one lane's f32x4
+    for (int o = threadIdx.x; o < MG * 64; o += 64 * KS) {
+        const int h = o >> 6, l = o & 63;
+        f32x4 sum[PP];
+#pragma unroll
+        for (int p = 0; p < PP; ++p) {
+            sum[p] = red[0][(h * PP + p) * 64 + l];
+#pragma unroll
+            for (int w = 1; w < KS; ++w) {
+                const f32x4 v = red[w][(h * PP + p) * 64 + l];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[p][e] += v[e];
+            }
+        }
+        const int64_t m = 16 * h + (l & 15), n = n0 + 4 * (l >> 4);
+        if (m >= a.M || n >= a.N) continue;
+        if (a.part) {                  // the gated sums as one part, for E4M3 rows
+#pragma unroll
+            for (int p = 0; p < PP; ++p) *reinterpret_cast<f32x4*>(a.part + (p * a.M + m) * a.ldp + n) = sum[p];
+            continue;
+        }
+        if constexpr (GATED)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[0][e] = act_value(a.act, sum[0][e]) * sum[1][e];
+        store_upto4(a.Y, m * a.ldy + n, a.N - n, a.y_dtype, sum[0]);
+    }
+}
+
+// Parts of a product in part order, the gate, and the output's type.  32 lanes to a row's block of 128 columns.
+template <bool GATED>
+__global__ __launch_bounds__(256) void scaled_sum_kernel(const ScaledArgs a, int64_t NBK) {
+    const int64_t id = (blockIdx.y * kGridX + blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t m = id / NBK, nb = id % NBK;
+    if (m >= a.M) return;
+    const int64_t n = nb * 128 + 4 * (threadIdx.x & 31);
+    const bool in = n < a.N;
+    constexpr int PP = GATED ? 2 : 1;
+    f32x4 sum[PP];
+#pragma unroll
+    for (int p = 0; p < PP; ++p) sum[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (in)
+        for (int k = 0; k < a.nsplit; ++k)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (((int64_t)k * PP + p) * a.M + m) * a.ldp + n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[p][e] = k ? sum[p][e] + v[e] : v[e];
+            }
+    if constexpr (GATED)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[0][e] = n + e < a.N ? act_value(a.act, sum[0][e]) * sum[1][e] : 0.f;
+    if (a.y_dtype == HTS_FP8_E4M3) {
+        float t = kLeastTop;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = fmaxf(t, fabsf(sum[0][e]));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
+        const float r = kE4m3Max / t;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = sum[0][e] * r;
+        if (in) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.Y) + m * a.ldy + n) = narrow4_e4m3(f);
+        if ((threadIdx.x & 31) == 0) a.ys[nb * a.ldys + m] = t / kE4m3Max;
+        return;
+    }
+    if (in) store_upto4(a.Y, m * a.ldy + n, a.N - n, a.y_dtype, sum[0]);
+}
+
+template <bool GATED, int MG>
+void launch_mg(const ScaledArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * 8);
+    scaled_stream_kernel<GATED, 8, 4, MG><<<grid, block, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s) {
+    if (a.gated) a.M <= 16 ? launch_mg<true, 1>(a, s) : launch_mg<true, 2>(a, s);
+    else a.M <= 16 ? launch_mg<false, 1>(a, s) : launch_mg<false, 2>(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_scaled_sum(const ScaledArgs& a, hipStream_t s) {
+    const int64_t NBK = scale_blocks(a.N);
+    const WideGrid wide = wide_grid((a.M * NBK + 7) / 8);
+    const dim3 grid(wide.x, wide.rest), block(256);
+    if (a.gated) scaled_sum_kernel<true><<<grid, block, 0, s>>>(a, NBK);
+    else scaled_sum_kernel<false><<<grid, block, 0, s>>>(a, NBK);
+    return hipGetLastError();
+}
+
+}  // namespace hts
