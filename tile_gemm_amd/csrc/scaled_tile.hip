@@ -28,15 +28,39 @@ __device__ __forceinline__ void copy4(const void* g, uint32_t lds_off) {
 // Past every buffer's end (their bytes stay below 2^31): such a lane reads zeros.
 constexpr uint32_t kOutside = 0x80000000u;
 
+// All but this wave's N youngest copies have landed and its LDS reads are back; then the same of the whole workgroup.
+template <int N>
+__device__ __forceinline__ void landed_but() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));      // lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <int WN, int WM, int BM>
 struct TileShape {
     static constexpr int NW = WN * WM, BN = 64 * WN, WTM = BM / WM, NBJ = WTM / 16;
     static constexpr int WJ = BN / (8 * NW), XJ = BM / (8 * NW);      // copies of 1 KB per wave and block
     static constexpr int XOFF = BN * 128, SOFF = XOFF + BM * 128, STAGE = SOFF + BM * 4;
     static constexpr int TOTAL = 2 * STAGE;
-    static_assert(BM % (8 * NW) == 0 && BM / 64 <= NW, "copies");
+    static constexpr int H = NBJ / 2;                     // a block's X: columns bj < H, then the others
+    static constexpr int PC = WJ + XJ / 2 + 1, QC = XJ / 2;   // copies per wave: W, X below H and scales; X from H on
+    static_assert(XJ % 2 == 0 && NBJ % 4 == 0 && BM / 64 <= NW && WTM / 16 % 2 == 0, "copies");
     static_assert(WN * BM * 4 <= STAGE, "the blocks' largest values fit");
 };
+
+// Workgroup id -> tile: each XCD (id % 8) takes a contiguous range of the order below, groups of kGroup tiles of W, W
+// fastest inside a group: the 32 workgroups that an XCD runs at once share W and X in its L2.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void block_of(int id, int NB, int MB, int& nb, int& mb) {
+    const int total = NB * MB, per = total / 8;
+    if (id < 8 * per) id = (id % 8) * per + id / 8;
+    const int grp = id / (kGroup * MB), in = id % (kGroup * MB), first = grp * kGroup;
+    const int n = NB - first < kGroup ? NB - first : kGroup;
+    nb = first + in % n;
+    mb = in / n;
+}
 
 template <bool GATED, int WN, int WM, int BM>
 __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const ScaledArgs a, int NB, int MB) {
@@ -45,7 +69,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % WN, wm = wave / WN;
-    const int nb = blockIdx.x % NB, mb = blockIdx.x / NB;
+    int nb, mb;
+    block_of(blockIdx.x, NB, MB, nb, mb);
     const int64_t n0 = (int64_t)nb * BNO, m0 = (int64_t)mb * BM;
     const int KB = (int)((a.K + 127) / 128);
     const int split = blockIdx.y;
@@ -59,6 +84,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     wr[0] = make_rsrc(a.W[0] + n0 * a.ldw[0], (uint32_t)((rows_n - 1) * a.ldw[0] + a.K));
     wr[1] = GATED ? make_rsrc(a.W[1] + n0 * a.ldw[1], (uint32_t)((rows_n - 1) * a.ldw[1] + a.K)) : wr[0];
     uint32_t wvo[T::WJ], xvo[T::XJ];
+    // first LDS row of X copy v: rows of the columns below H come first
+    auto x_row = [&](int v) {
+        const int r = 8 * (wave + NW * (v % T::QC)), half = T::WTM / 2;
+        return r / half * T::WTM + r % half + (v >= T::QC ? half : 0);
+    };
 #pragma unroll
     for (int v = 0; v < T::WJ; ++v) {
         const int job = wave + NW * v, r = 8 * job + (lane >> 3);     // LDS row: wave r / 64's row r % 64
@@ -70,27 +100,30 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
 #pragma unroll
     for (int v = 0; v < T::XJ; ++v) {
         // column j of a wave's block bj is its row NBJ j + bj, so that a lane's scales are consecutive
-        const int r = 8 * (wave + NW * v) + (lane >> 3);
-        const int t = r % T::WTM;
-        int m = r / T::WTM * T::WTM + NBJ * (t & 15) + (t >> 4);
+        const int t = x_row(v) + (lane >> 3);
+        int m = t / T::WTM * T::WTM + NBJ * (t & 15) + t % T::WTM / 16;
         m = m < rows_m ? m : rows_m - 1;
         xvo[v] = (uint32_t)(m * a.ldx) + 16 * ch;
     }
-    const int sm = 64 * wave + lane;
+    const int sj = wave % (BM / 64), sm = 64 * sj + lane;             // (copied by more than one wave, the same values)
     const float* xs = a.xs + m0 + (sm < rows_m ? sm : rows_m - 1);
     const int tail = (int)(a.K - (int64_t)128 * (KB - 1));            // columns of the last block
 
-    auto issue = [&](int kb) {
-        const uint32_t st = (kb & 1) * T::STAGE, so = 128u * kb;
-        const bool cut = kb == KB - 1 && 16 * ch >= tail;
-#pragma unroll
-        for (int v = 0; v < T::WJ; ++v) {
-            const int job = wave + NW * v;
-            copy16(wr[GATED ? (job >> 2) & 1 : 0], st + 1024 * job, cut ? kOutside : wvo[v], so);
+    // copy c of block kb: W, X below H, the scales (0 .. PC - 1), X from H on (PC .. PC + QC - 1).  Past the last block
+    // of this part the copies stay, so that as many are in flight in every step, but read zeros from outside
+    // (the scales: once more the last ones).
+    auto outside = [&](int kb) { return 16 * ch >= (kb >= kb1 ? 0 : kb == KB - 1 ? tail : 128); };
+    auto copy = [&](int kb, int c, bool cut) {
+        const uint32_t st = (kb & 1) * T::STAGE, so = kb < kb1 ? 128u * kb : 0u;
+        if (c < T::WJ) {
+            const int job = wave + NW * c;
+            copy16(wr[GATED ? (job >> 2) & 1 : 0], st + 1024 * job, cut ? kOutside : wvo[c], so);
+        } else if (c == T::PC - 1) {
+            copy4(xs + (int64_t)(kb < kb1 ? kb : kb1 - 1) * a.ldxs, st + T::SOFF + 256 * sj);
+        } else {
+            const int v = c < T::PC ? c - T::WJ : c - T::PC + T::QC;
+            copy16(xr, st + T::XOFF + 128 * x_row(v), cut ? kOutside : xvo[v], so);
         }
-#pragma unroll
-        for (int v = 0; v < T::XJ; ++v) copy16(xr, st + T::XOFF + 1024 * (wave + NW * v), cut ? kOutside : xvo[v], so);
-        if (wave < BM / 64) copy4(xs + (int64_t)kb * a.ldxs, st + T::SOFF + 256 * wave);
     };
 
     f32x4 acc[4][NBJ];
@@ -107,40 +140,91 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
         const int k = kb + lane < KB ? kb + lane : KB - 1;
         wsv[0] = a.ws[0][srow * a.ldws[0] + k];
         if (GATED) wsv[1] = a.ws[1][srow * a.ldws[1] + k];
+        // taken here: read at its first use, the wait for it would be one for every copy in flight, in every block
+        asm volatile("" : "+v"(wsv[0]), "+v"(wsv[1]));
     };
     const int i = lane & 15, g = lane >> 4;
     const int c0 = 16 * (g ^ ((i >> 1) & 7)), c1 = 16 * ((4 + g) ^ ((i >> 1) & 7));
     const uint32_t abase = wn * 8192 + i * 128, bbase = T::XOFF + wm * T::WTM * 128 + i * 128;
     const uint32_t sbase = T::SOFF + 4 * (wm * T::WTM + NBJ * i);
 
-    if (kb0 < kb1) issue(kb0);
+    // One block's sums: step t = 4 bj + b makes the piece (b, bj) and adds the scaled piece of step t - 3, whose matrix
+    // instruction has ended by then.  B of step bj + 1 is read during step bj; the next block's A, first B and scales
+    // during the last step.  Two barriers a block say what has landed and what has been read by all: one before the first
+    // read of the columns from H on, behind which the places of W, of the other columns and of the scales are free, and
+    // one before the next block's first reads.  So every copy is issued more than a block's time before it is needed.
+    auto read_a = [&](uint32_t st, int b) { return cat8(ld16(smem + st + abase + 2048 * b + c0), ld16(smem + st + abase + 2048 * b + c1)); };
+    auto read_b = [&](uint32_t st, int bj) { return cat8(ld16(smem + st + bbase + 2048 * bj + c0), ld16(smem + st + bbase + 2048 * bj + c1)); };
+    u32x8 A[4], B;
+    float sx[NBJ];
+    f32x4 p[4];
+    float s0 = 0.f, s1 = 0.f;          // scales of the pieces not yet added
+#pragma unroll
+    for (int b = 0; b < 4; ++b) p[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int b, int bj, float s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][bj][e] = __builtin_fmaf(p[b][e], s, acc[b][bj][e]);
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < T::PC + T::QC; ++c) copy(kb0 + k, c, outside(kb0 + k));
+    landed_but<T::PC + 2 * T::QC>();
+    {
+        const uint32_t st = (kb0 & 1) * T::STAGE;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) A[b] = read_a(st, b);
+        B = read_b(st, 0);
+#pragma unroll
+        for (int bj = 0; bj < NBJ; ++bj) sx[bj] = *reinterpret_cast<const float*>(smem + st + sbase + 4 * bj);
+    }
     for (int kb = kb0; kb < kb1; ++kb) {
         if (((kb - kb0) & 63) == 0) load_ws(kb);
-        __syncthreads();               // this block's copies have landed, and the other stage is free
-        if (kb + 1 < kb1) issue(kb + 1);
-        const uint8_t* st = smem + (kb & 1) * T::STAGE;
+        const bool cut = outside(kb + 2);
+        const uint32_t st = (kb & 1) * T::STAGE, sn = T::STAGE - st;
         const int l = (kb - kb0) & 63;
         const float w0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[0]), l));
         const float w1 = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[1]), l)) : w0;
-        float sx[NBJ];
-#pragma unroll
-        for (int bj = 0; bj < NBJ; ++bj) sx[bj] = *reinterpret_cast<const float*>(st + sbase + 4 * bj);
-        u32x8 A[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) A[b] = cat8(ld16(st + abase + 2048 * b + c0), ld16(st + abase + 2048 * b + c1));
+        float sxn[NBJ];
 #pragma unroll
         for (int bj = 0; bj < NBJ; ++bj) {
-            const u32x8 B = cat8(ld16(st + bbase + 2048 * bj + c0), ld16(st + bbase + 2048 * bj + c1));
-            const float s0 = sx[bj] * w0, s1 = GATED ? sx[bj] * w1 : s0;
+            u32x8 Bn;
+            if (bj == T::H - 1) landed_but<T::PC + T::QC>();   // X from H on is in; everyone has read the rest
+            if (bj + 1 < NBJ) {
+                Bn = read_b(st, bj + 1);
+            } else {                       // the next block's W, first X and scales are in; everyone has read this block
+                landed_but<T::PC + T::QC>();
+                Bn = read_b(sn, 0);
+#pragma unroll
+                for (int c = 0; c < NBJ; ++c) sxn[c] = *reinterpret_cast<const float*>(smem + sn + sbase + 4 * c);
+            }
+            const float t0 = sx[bj] * w0, t1 = GATED ? sx[bj] * w1 : t0;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const f32x4 p = mfma_block(A[b], B);
-                const float s = (GATED && b >= 2) ? s1 : s0;
+                const int last = bj == 0 ? NBJ - 1 : bj - 1;
+                p[b] = mfma_block(A[b], B);
+                if (bj + 1 == NBJ) A[b] = read_a(sn, b);
+                // the copies of block kb + 2 go between the matrix instructions, into what has been read
+                constexpr int FIRST = T::H - 1, SLOTS = 4 * (NBJ - T::H);
+                const int slot = 4 * (bj - FIRST) + b;
+                if (slot >= 0 && slot < SLOTS)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[b][bj][e] = __builtin_fmaf(p[e], s, acc[b][bj][e]);
+                    for (int c = T::PC * slot / SLOTS; c < T::PC * (slot + 1) / SLOTS; ++c) copy(kb + 2, c, cut);
+                if (bj + 1 == NBJ && b < T::QC) copy(kb + 2, T::PC + b, cut);
+                if (b < 3) add(b + 1, last, (GATED && b + 1 >= 2) ? s1 : s0);
+                else add(0, bj, t0);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            s0 = t0;
+            s1 = t1;
+            B = Bn;
         }
+#pragma unroll
+        for (int bj = 0; bj < NBJ; ++bj) sx[bj] = sxn[bj];
     }
+#pragma unroll
+    for (int b = 1; b < 4; ++b) add(b, NBJ - 1, (GATED && b >= 2) ? s1 : s0);
+    __syncthreads();                   // no copy is left in flight: LDS is free
 
     // lane (j + 16 q) holds rows 4 q .. 4 q + 3 of block b for row NBJ j + bj of X
     const int64_t m1 = m0 + wm * T::WTM + NBJ * i;
@@ -169,7 +253,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
                 }
         if constexpr (BNO == 128) {
             if (a.y_dtype == HTS_FP8_E4M3) {
-                __syncthreads();       // the last block's reads are done: its memory takes the largest values
                 float* tops = reinterpret_cast<float*>(smem);
                 float t[NBJ];
 #pragma unroll
