@@ -519,7 +519,7 @@ enum { HTS_ACT_SILU = 0, HTS_ACT_GELU = 1, HTS_ACT_GELU_TANH = 2 };
  *   h_dtype HTS_F32, HTS_F16, HTS_BF16 : h_scale must be NULL; ldh >= N a multiple of 4, any N
  *   h_dtype HTS_FP8_E4M3               : H rows of values and h_scale [ceil(N/128), ldhs] as hts_quantize_rows makes
  *                                        them of the unrounded H; N and ldh multiples of 16.  The next product's X.
- * workspace: hts_scaled_gated_workspace() bytes; optional except where h_dtype is HTS_FP8_E4M3 and M is at most 32
+ * workspace: hts_scaled_gated_workspace() bytes; optional, but for HTS_FP8_E4M3, which may need all of them
  * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm. */
 hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
                             const float* x_scale, int64_t ldxs, const hts_scaled_weight* gate,

@@ -22,7 +22,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["hts_api.cpp", "pack.hip", "gemm_decode.hip", "gemm_prefill.hip", "wanda.hip", "elementwise.hip",
            "serve_api.cpp", "kv_step.hip", "rope.hip", "attn_decode.hip", "norm.hip",
-           "scaled_api.cpp", "quant.hip", "scaled_stream.hip", "scaled_tile.hip"]
+           "scaled_api.cpp", "quant.hip", "scaled_stream.hip", "scaled_ring.hip", "scaled_tile.hip"]
 
 ARCH = "gfx950"
 COMMON = [

@@ -79,23 +79,83 @@ hts_status check_act(int32_t act) {
 bool is_out(int32_t dt) { return dt == HTS_F32 || is16bit(dt); }
 int out_bytes(int32_t dt) { return dt == HTS_F32 ? 4 : dt == HTS_FP8_E4M3 ? 1 : 2; }
 
-// How a product runs: streaming, or tiled in workgroups of `tile`, over `nsplit` parts of K.
+// How a product runs: which kernel, over how many parts of K, with what workspace.
 struct Plan {
-    bool stream;
-    hts::ScaledTile tile;
+    hts::ScaledKernel kernel;
     int32_t nsplit;
     int64_t ldp;
     uint64_t bytes;        // of the parts
     bool need;             // no run without them
 };
+
+// The kernel and split with the least estimated time.  A kernel's step (`blocks` of K on rows_n x rows_m) takes `step` us
+// with one workgroup on each of some CUs, and no less than its weights take from memory at 6.5 TB/s; workgroups beyond a
+// CU's each (two: TILE_128x128) wait for another round.  Measured steps, and the kernels against one another (us, in
+// the order of their rows of X): the table in the comment of each kernel file.
+struct Shape {
+    int rows_n, rows_m, blocks;
+    float step;
+};
+constexpr Shape kShapes[hts::SCALED_KERNELS] = {
+    {16, 32, 8, 0.0f},         // SCALED_STREAM (its own estimate)
+    {32, 16, 8, 0.55f},        // RING_32x16
+    {64, 16, 2, 0.22f},        // RING_64x16
+    {32, 32, 4, 0.42f},        // RING_32x32
+    {64, 32, 2, 0.31f},        // RING_64x32
+    {64, 64, 2, 0.58f},        // RING_64x64
+    {128, 64, 2, 0.70f},       // RING_128x64
+    {128, 128, 1, 0.60f},      // TILE_128x128
+    {256, 128, 1, 1.10f},      // TILE_256x128
+    {256, 256, 1, 1.05f},      // TILE_256x256
+};
+constexpr float kBytesPerUs = 6.5e6f;
+
+float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weights, int split) {
+    if (k == hts::SCALED_STREAM)
+        return 4.0f + std::max(weights * (float)N * KB * 128 / 5.5e6f * (1.0f + M / 40.0f),
+                               0.35f * (weights + (M + 15) / 16) * ((KB + 7) / 8));     // a wave's loads, one block at a time
+    const Shape& s = kShapes[k];
+    const int64_t mb = (M + s.rows_m - 1) / s.rows_m;
+    const int64_t tiles = (N * weights + s.rows_n - 1) / s.rows_n * mb * split;
+    const int64_t steps = ((KB + split - 1) / split + s.blocks - 1) / s.blocks;
+    const int at_once = k == hts::TILE_128x128 ? 512 : 256;
+    float us = 3.5f;
+    const int64_t whole = tiles / at_once;
+    for (int last = 0; last < 2; ++last) {
+        const int64_t busy = last ? tiles % at_once : at_once, rounds = last ? (busy ? 1 : 0) : whole;
+        if (!rounds) continue;
+        float step = s.step;
+        if (k == hts::TILE_128x128 && busy > 256) step = 1.2f;             // two on a CU
+        if (k == hts::TILE_256x256) step += 0.9f * busy / 256;             // what the matrix cores' clock and L2 leave
+        const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / kBytesPerUs;
+        us += rounds * ((k < hts::TILE_128x128 ? 2.0f : 4.5f) + steps * std::max(step, wait));
+    }
+    return us;
+}
+
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool out8) {
     Plan p{};
-    p.nsplit = 1;
     p.ldp = (N + 3) / 4 * 4;
-    p.stream = M <= hts::kScaledStreamRows;
-    p.need = p.stream && out8;
-    p.tile = hts::TILE_256x256;
-    if (p.nsplit > 1 || p.need) p.bytes = (uint64_t)p.nsplit * (gated ? 2 : 1) * M * p.ldp * 4;
+    const int64_t KB = scale_blocks(K);
+    const int weights = gated ? 2 : 1;
+    const float plane = (float)weights * M * p.ldp * 4 / 4.0e6f;           // a part written and read, us
+    float best = 0.0f;
+    for (int i = 0; i < hts::SCALED_KERNELS; ++i) {
+        const auto k = (hts::ScaledKernel)i;
+        if (k == hts::SCALED_STREAM && M > hts::kScaledStreamRows) continue;
+        for (int split = 1; split <= 8; split *= 2) {
+            if (split > KB || (split > 1 && k == hts::SCALED_STREAM)) break;
+            const bool parts = split > 1 || (out8 && !hts::writes_e4m3(k));
+            const float us = estimate(k, M, N, KB, weights, split) + (parts ? 3.0f + split * plane : 0.0f);
+            if (!p.nsplit || us < best) {
+                best = us;
+                p.kernel = k;
+                p.nsplit = split;
+                p.need = out8 && !hts::writes_e4m3(k);
+                p.bytes = parts ? (uint64_t)split * weights * M * p.ldp * 4 : 0;
+            }
+        }
+    }
     return p;
 }
 
@@ -107,7 +167,9 @@ hts_status run(hts::ScaledArgs& a, const Plan& p, void* workspace, size_t worksp
     } else {
         a.nsplit = 1;
     }
-    hipError_t e = p.stream ? hts::launch_scaled_stream(a, s) : hts::launch_scaled_tile(a, p.tile, s);
+    hipError_t e = p.kernel == hts::SCALED_STREAM     ? hts::launch_scaled_stream(a, s)
+                   : p.kernel <= hts::RING_128x64 ? hts::launch_scaled_ring(a, p.kernel, s)
+                                                  : hts::launch_scaled_tile(a, p.kernel, s);
     if (e == hipSuccess && a.part) e = hts::launch_scaled_sum(a, s);
     return hip_status(e, "scaled product kernel launch");
 }

@@ -45,18 +45,27 @@ struct ScaledArgs {
     int32_t y_dtype;           // HTS_F32, HTS_F16, HTS_BF16, or HTS_FP8_E4M3 with ys (gated)
     float* ys;                 // [blocks of N][ldys], entry m
     int64_t ldys;
-    // nsplit > 1: the blocks of K are cut into nsplit parts; part p of weight w goes to part[(p * weights + w) * M * ldp]
+    // part not NULL: the blocks of K are cut into nsplit parts, the 32-bit sums of part p and weight w go to
+    // part[(p * weights + w) * M * ldp], and launch_scaled_sum makes Y of them
     float* part;
     int64_t ldp;
     int32_t nsplit;
 };
 
-// Rows of X up to which a product streams its weights past them.
+// The kernels of a product.  Streaming: 16 outputs a workgroup, up to kScaledStreamRows rows.  RING_*, TILE_*: rows of W
+// (gated: half of them gate, half up) x rows of X a workgroup.
 constexpr int64_t kScaledStreamRows = 32;
+enum ScaledKernel {
+    SCALED_STREAM = 0,
+    RING_32x16, RING_64x16, RING_32x32, RING_64x32, RING_64x64, RING_128x64,
+    TILE_128x128, TILE_256x128, TILE_256x256,
+    SCALED_KERNELS
+};
+// Those whose workgroups hold whole blocks of 128 outputs make E4M3 rows themselves; the others leave their sums in a.part.
+inline bool writes_e4m3(ScaledKernel k) { return k == TILE_256x128 || k == TILE_256x256; }
 hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s);
-// Tile shapes: rows of W and of X a workgroup.
-enum ScaledTile { TILE_256x256 = 0, TILE_256x128 = 1, TILE_128x128 = 2 };
-hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledTile shape, hipStream_t s);
+hipError_t launch_scaled_ring(const ScaledArgs& a, ScaledKernel k, hipStream_t s);
+hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledKernel k, hipStream_t s);
 // The sum of a.nsplit parts, gated and rounded to Y.
 hipError_t launch_scaled_sum(const ScaledArgs& a, hipStream_t s);
 

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     const int64_t n0 = (int64_t)nb * BNO, m0 = (int64_t)mb * BM;
     const int KB = (int)((a.K + 127) / 128);
     const int split = blockIdx.y;
-    const int kb0 = (int)((int64_t)split * KB / a.nsplit), kb1 = (int)((int64_t)(split + 1) * KB / a.nsplit);
+    const int kb0 = split * KB / a.nsplit, kb1 = (split + 1) * KB / a.nsplit;
 
     // copies: a lane takes chunk `ch` of a row; LDS chunk position = chunk ^ ((row / 2) & 7)
     const int ch = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
 
     // lane (j + 16 q) holds rows 4 q .. 4 q + 3 of block b for row NBJ j + bj of X
     const int64_t m1 = m0 + wm * T::WTM + NBJ * i;
-    if (a.nsplit > 1) {
+    if (a.part) {
         const int64_t plane = a.M * a.ldp;
         float* part = a.part + (int64_t)split * (GATED ? 2 : 1) * plane;
 #pragma unroll
@@ -316,10 +316,12 @@ hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledTile shape, hipStream_t s) {
-    if (shape == TILE_256x256) return a.gated ? launch_shape<true, 4, 2, 256>(a, s) : launch_shape<false, 4, 2, 256>(a, s);
-    if (shape == TILE_256x128) return a.gated ? launch_shape<true, 4, 2, 128>(a, s) : launch_shape<false, 4, 2, 128>(a, s);
-    return a.gated ? launch_shape<true, 2, 2, 128>(a, s) : launch_shape<false, 2, 2, 128>(a, s);
+hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledKernel k, hipStream_t s) {
+    if (a.y_dtype == HTS_FP8_E4M3 && !a.part && !writes_e4m3(k)) return hipErrorInvalidValue;
+    if (k == TILE_256x256) return a.gated ? launch_shape<true, 4, 2, 256>(a, s) : launch_shape<false, 4, 2, 256>(a, s);
+    if (k == TILE_256x128) return a.gated ? launch_shape<true, 4, 2, 128>(a, s) : launch_shape<false, 4, 2, 128>(a, s);
+    if (k == TILE_128x128) return a.gated ? launch_shape<true, 2, 2, 128>(a, s) : launch_shape<false, 2, 2, 128>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace hts
