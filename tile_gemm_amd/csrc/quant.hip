@@ -10,41 +10,6 @@
 namespace hts {
 namespace {
 
-// 16 consecutive values at column c of a row (c and K multiples of 16), as floats.
-template <int DT>
-__device__ __forceinline__ void load16(const void* row, int64_t c, float (&f)[16]) {
-    if constexpr (DT == HTS_F32) {
-        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4 v = p[i];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * i + e] = v[e];
-        }
-    } else {
-        using T = typename std::conditional<DT == HTS_BF16, BF16T, F16T>::type;
-        const uint16_t* p = static_cast<const uint16_t*>(row) + c;
-        widen8<T>(ld16(p), f);
-        widen8<T>(ld16(p + 8), f + 8);
-    }
-}
-
-__device__ __forceinline__ float top16(const float (&f)[16]) {
-    float t = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) t = fmaxf(t, fabsf(f[e]));
-    return t;
-}
-
-__device__ __forceinline__ u32x4 scaled16(float (&f)[16], float r) {
-    u32x4 q;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] *= r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = narrow4_e4m3(f + 4 * i);
-    return q;
-}
-
 // Eight lanes to a block of a row, 16 values each; a workgroup's 32 blocks run along the row.
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a, int64_t KB) {
@@ -55,11 +20,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a, i
     const bool in = c < a.K;
     float f[16] = {};
     constexpr int ES = DT == HTS_F32 ? 4 : 2;
-    if (in) load16<DT>(static_cast<const uint8_t*>(a.X) + m * a.ldx * ES, c, f);
-    float t = top16(f);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
-    t = fmaxf(t, kLeastTop);
+    if (in) load_values16<DT>(static_cast<const uint8_t*>(a.X) + m * a.ldx * ES, c, f);
+    const float t = block_top(f);
     if (in) st16(a.Q + m * a.ldq + c, scaled16(f, kE4m3Max / t));
     if ((threadIdx.x & 7) == 0) a.S[kb * a.lds + m] = t / kE4m3Max;
 }
@@ -79,7 +41,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(const QuantArgs a,
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
         const int64_t n = row0 + 32 * v;
-        if (n < a.M && c < a.K) load16<DT>(static_cast<const uint8_t*>(a.X) + n * a.ldx * ES, c, f[v]);
+        if (n < a.M && c < a.K) load_values16<DT>(static_cast<const uint8_t*>(a.X) + n * a.ldx * ES, c, f[v]);
         t = fmaxf(t, top16(f[v]));
     }
 #pragma unroll

@@ -210,6 +210,7 @@ uint64_t round256(uint64_t n) { return (n + 255) & ~uint64_t(255); }
 
 // The workspace of a feed-forward part: the quantised rows and inner rows, then what the products take.
 struct MlpPlan {
+    bool made;             // two launches: each quantises its own input (then `parts` holds the 32-bit inner rows)
     Plan gated, down;
     int64_t lds;
     uint64_t xs, hq, hs, parts, bytes;       // offsets; the rows of X come first
@@ -224,6 +225,11 @@ MlpPlan mlp_plan(int64_t M, int64_t hidden, int64_t inner) {
     p.hs = p.hq + round256((uint64_t)M * inner);
     p.parts = p.hs + round256(4 * (uint64_t)p.lds * scale_blocks(inner));
     p.bytes = p.parts + std::max(p.gated.bytes, p.down.bytes);
+    p.made = M <= hts::kMadeRows && M * scale_blocks(hidden) <= hts::kMadeBlocks && M * scale_blocks(inner) <= hts::kMadeBlocks;
+    if (p.made) {
+        p.parts = 0;
+        p.bytes = round256(4 * (uint64_t)M * inner);
+    }
     return p;
 }
 
@@ -352,32 +358,43 @@ hts_status hts_scaled_mlp(int32_t act, int32_t dtype, int64_t M, int64_t hidden,
     uint8_t* w = static_cast<uint8_t*>(workspace);
     float *xs = reinterpret_cast<float*>(w + p.xs), *hs = reinterpret_cast<float*>(w + p.hs);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const hts::QuantArgs q{dtype, M, hidden, X, ldx, w, hidden, xs, p.lds};
-    if ((st = hip_status(hts::launch_quantize_rows(q, s), "quantizer kernel launch"))) return st;
     hts::ScaledArgs a{};
     a.M = M;
     a.N = inner;
     a.K = hidden;
-    set_rows(a, w, hidden, xs, p.lds);
     set_weight(a, 0, *gate);
     set_weight(a, 1, *up);
     a.act = act;
     a.gated = 1;
+    a.nsplit = 1;
+    hts::ScaledArgs d{};
+    d.M = M;
+    d.N = hidden;
+    d.K = inner;
+    set_weight(d, 0, *down);
+    d.Y = Y;
+    d.ldy = ldy;
+    d.y_dtype = dtype;
+    d.nsplit = 1;
+    if (p.made) {
+        set_rows(a, X, ldx, nullptr, 0);
+        a.Y = w;
+        a.ldy = inner;
+        a.y_dtype = HTS_F32;
+        if ((st = hip_status(hts::launch_scaled_stream_made(a, dtype, s), "scaled product kernel launch"))) return st;
+        set_rows(d, w, inner, nullptr, 0);
+        return hip_status(hts::launch_scaled_stream_made(d, HTS_F32, s), "scaled product kernel launch");
+    }
+    const hts::QuantArgs q{dtype, M, hidden, X, ldx, w, hidden, xs, p.lds};
+    if ((st = hip_status(hts::launch_quantize_rows(q, s), "quantizer kernel launch"))) return st;
+    set_rows(a, w, hidden, xs, p.lds);
     a.Y = w + p.hq;
     a.ldy = inner;
     a.y_dtype = HTS_FP8_E4M3;
     a.ys = hs;
     a.ldys = p.lds;
     if ((st = run(a, p.gated, w + p.parts, p.gated.bytes, s))) return st;
-    hts::ScaledArgs d{};
-    d.M = M;
-    d.N = hidden;
-    d.K = inner;
     set_rows(d, w + p.hq, inner, hs, p.lds);
-    set_weight(d, 0, *down);
-    d.Y = Y;
-    d.ldy = ldy;
-    d.y_dtype = dtype;
     return run(d, p.down, w + p.parts, p.down.bytes, s);
 }
 

@@ -1,6 +1,8 @@
 // Device pieces of the block-scaled 8-bit kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_common.h"
 #include "scaled_internal.h"
 #include "serve_device.h"
@@ -25,6 +27,51 @@ __device__ __forceinline__ float act_value(int act, float g) {
 __device__ __forceinline__ f32x4 mfma_block(u32x8 a, u32x8 b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_bit_cast(i32x8, a), __builtin_bit_cast(i32x8, b),
                                                             f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// ---- rows to E4M3 ----
+
+// 16 consecutive values at column c of a row (c and K multiples of 16), as floats.
+template <int DT>
+__device__ __forceinline__ void load_values16(const void* row, int64_t c, float (&f)[16]) {
+    if constexpr (DT == HTS_F32) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 v = p[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * i + e] = v[e];
+        }
+    } else {
+        using T = typename std::conditional<DT == HTS_BF16, BF16T, F16T>::type;
+        const uint16_t* p = static_cast<const uint16_t*>(row) + c;
+        widen8<T>(ld16(p), f);
+        widen8<T>(ld16(p + 8), f + 8);
+    }
+}
+
+__device__ __forceinline__ float top16(const float (&f)[16]) {
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) t = fmaxf(t, fabsf(f[e]));
+    return t;
+}
+
+__device__ __forceinline__ u32x4 scaled16(float (&f)[16], float r) {
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] *= r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = narrow4_e4m3(f + 4 * i);
+    return q;
+}
+
+// A block's largest magnitude from its eight lanes' values, and at least kLeastTop.
+__device__ __forceinline__ float block_top(const float (&f)[16]) {
+    float t = top16(f);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
+    return fmaxf(t, kLeastTop);
 }
 
 // Up to four consecutive outputs of a row from column n on, those below N.

@@ -64,6 +64,10 @@ enum ScaledKernel {
 // Those whose workgroups hold whole blocks of 128 outputs make E4M3 rows themselves; the others leave their sums in a.part.
 inline bool writes_e4m3(ScaledKernel k) { return k == TILE_256x128 || k == TILE_256x256; }
 hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s);
+// The same on rows that its workgroups make themselves (a.X in x_dtype, a.xs unused): gated of HTS_F16 or HTS_BF16 rows, plain
+// of HTS_F32 rows.  Few rows, and few blocks of them: they lie in LDS.
+constexpr int64_t kMadeRows = 4, kMadeBlocks = 384;
+hipError_t launch_scaled_stream_made(const ScaledArgs& a, int32_t x_dtype, hipStream_t s);
 hipError_t launch_scaled_ring(const ScaledArgs& a, ScaledKernel k, hipStream_t s);
 hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledKernel k, hipStream_t s);
 // The sum of a.nsplit parts, gated and rounded to Y.

@@ -19,10 +19,15 @@ __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) 
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
 
-template <bool GATED, int KS, int NT, int MG>
+// XT: the type of X.  HTS_FP8_E4M3: rows and scales as hts_quantize_rows makes them.  Others: every workgroup makes them
+// itself, in LDS, while its first weights are on their way.
+template <bool GATED, int KS, int NT, int MG, int XT>
 __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs a) {
     constexpr int PP = GATED ? 2 : 1;
+    constexpr bool MAKE = XT != HTS_FP8_E4M3;
+    static_assert(!MAKE || MG == 1, "few rows");
     __shared__ f32x4 red[KS][MG * PP * 64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t made[];        // M rows of KB blocks, then their scales
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -36,14 +41,15 @@ __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs
         wr[p] = make_rsrc(a.W[p] + n0 * a.ldw[p], (uint32_t)((rows - 1) * a.ldw[p] + a.K));
         wvo[p] = (uint32_t)((i < rows ? i : rows - 1) * a.ldw[p]) + 16 * g;
     }
-    const rsrc_t xr = make_rsrc(a.X, (uint32_t)((a.M - 1) * a.ldx + a.K));
+    const rsrc_t xr = make_rsrc(a.X, MAKE ? 0u : (uint32_t)((a.M - 1) * a.ldx + a.K));
     uint32_t xvo[MG];
     const float* xs[MG];
+    float* made_s = reinterpret_cast<float*>(made + a.M * KB * 128);
 #pragma unroll
     for (int h = 0; h < MG; ++h) {
         const int m = 16 * h + i < (int)a.M ? 16 * h + i : (int)a.M - 1;
-        xvo[h] = (uint32_t)(m * a.ldx) + 16 * g;
-        xs[h] = a.xs + m;
+        xvo[h] = MAKE ? (uint32_t)(m * KB * 128) + 16 * g : (uint32_t)(m * a.ldx) + 16 * g;
+        xs[h] = MAKE ? made_s + m * KB : a.xs + m;
     }
     const int tail = (int)(a.K - (int64_t)128 * (KB - 1));
     const float* ws[PP];
@@ -56,28 +62,56 @@ __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs
 #pragma unroll
         for (int p = 0; p < PP; ++p) acc[h][p] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int t = wave; t < KB; t += NT * KS) {
-        u32x4 W[NT][PP][2], X[NT][MG][2];
-        float sx[NT][MG], sw[NT][PP];
+    u32x4 W[NT][PP][2], X[NT][MG][2];
+    float sx[NT][MG], sw[NT][PP];
+    auto load_w = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
         for (int s = 0; s < NT; ++s) {
             if (t + KS * s >= KB) break;
             const int kb = t + KS * s;
-            const bool cut = kb == KB - 1;
-            const uint32_t so = 128u * kb;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const bool out = cut && 16 * (g + 4 * u) >= tail;
+                const bool out = kb == KB - 1 && 16 * (g + 4 * u) >= tail;
 #pragma unroll
-                for (int p = 0; p < PP; ++p) W[s][p][u] = load16(wr[p], out ? kOutside : wvo[p] + 64 * u, so);
-#pragma unroll
-                for (int h = 0; h < MG; ++h) X[s][h][u] = load16(xr, out ? kOutside : xvo[h] + 64 * u, so);
+                for (int p = 0; p < PP; ++p) W[s][p][u] = load16(wr[p], out ? kOutside : wvo[p] + 64 * u, 128u * kb);
             }
-#pragma unroll
-            for (int h = 0; h < MG; ++h) sx[s][h] = xs[h][kb * a.ldxs];
 #pragma unroll
             for (int p = 0; p < PP; ++p) sw[s][p] = ws[p][kb];
         }
+    };
+    auto load_x = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < NT; ++s) {
+            if (t + KS * s >= KB) break;
+            const int kb = t + KS * s;
+#pragma unroll
+            for (int h = 0; h < MG; ++h) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if constexpr (MAKE) X[s][h][u] = ld16(made + xvo[h] + 128 * kb + 64 * u);
+                    else X[s][h][u] = load16(xr, kb == KB - 1 && 16 * (g + 4 * u) >= tail ? kOutside : xvo[h] + 64 * u, 128u * kb);
+                }
+                sx[s][h] = xs[h][MAKE ? kb : kb * a.ldxs];
+            }
+        }
+    };
+    if constexpr (MAKE) {
+        // eight lanes to a block, as in hts_quantize_rows; columns past K are zeros
+        load_w(wave);
+        constexpr int ES = XT == HTS_F32 ? 4 : 2;
+        for (int id = threadIdx.x >> 3; id < (int)a.M * KB; id += 8 * KS) {
+            const int m = id / KB, kb = id % KB, c = kb * 128 + 16 * (threadIdx.x & 7);
+            float f[16] = {};
+            if (c < a.K) load_values16<XT>(a.X + m * a.ldx * ES, c, f);
+            const float top = block_top(f);
+            st16(made + (int64_t)id * 128 + 16 * (threadIdx.x & 7), scaled16(f, kE4m3Max / top));
+            if ((threadIdx.x & 7) == 0) made_s[id] = top / kE4m3Max;
+        }
+        __syncthreads();
+    }
+    for (int t = wave; t < KB; t += NT * KS) {
+        if (!MAKE || t != wave) load_w(t);
+        load_x(t);
 #pragma unroll
         for (int s = 0; s < NT; ++s) {
             if (t + KS * s >= KB) break;
@@ -165,17 +199,20 @@ __global__ __launch_bounds__(256) void scaled_sum_kernel(const ScaledArgs a, int
     if (in) store_upto4(a.Y, m * a.ldy + n, a.N - n, a.y_dtype, sum[0]);
 }
 
-template <bool GATED, int NT, int MG>
+constexpr int kWaves = 8;
+// Four blocks of loads ahead where a wave has as many (4096 x 11008, one row: 12.1 us against 12.5 with one ahead).
+inline bool far_ahead(int64_t K) { return K > kWaves * 4 * 128; }
+
+template <bool GATED, int NT, int MG, int XT>
 hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
-    constexpr int KS = 8;
-    const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * KS);
-    scaled_stream_kernel<GATED, KS, NT, MG><<<grid, block, 0, s>>>(a);
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kWaves);
+    const size_t lds = XT == HTS_FP8_E4M3 ? 0 : a.M * scale_blocks(a.K) * (128 + 4);
+    scaled_stream_kernel<GATED, kWaves, NT, MG, XT><<<grid, block, lds, s>>>(a);
     return hipGetLastError();
 }
-template <bool GATED, int MG>
+template <bool GATED, int MG, int XT = HTS_FP8_E4M3>
 hipError_t launch_mg(const ScaledArgs& a, hipStream_t s) {
-    // Four blocks of loads ahead where a wave has as many (4096 x 11008, one row: 12.1 us against 12.5 with one ahead).
-    return a.K > 8 * 4 * 128 ? launch_rows<GATED, 4, MG>(a, s) : launch_rows<GATED, 1, MG>(a, s);
+    return far_ahead(a.K) ? launch_rows<GATED, 4, MG, XT>(a, s) : launch_rows<GATED, 1, MG, XT>(a, s);
 }
 
 }  // namespace
@@ -184,6 +221,12 @@ hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s) {
     if (a.M > kScaledStreamRows || (a.y_dtype == HTS_FP8_E4M3 && !a.part)) return hipErrorInvalidValue;
     if (a.gated) return a.M <= 16 ? launch_mg<true, 1>(a, s) : launch_mg<true, 2>(a, s);
     return a.M <= 16 ? launch_mg<false, 1>(a, s) : launch_mg<false, 2>(a, s);
+}
+
+hipError_t launch_scaled_stream_made(const ScaledArgs& a, int32_t x_dtype, hipStream_t s) {
+    if (a.M > kMadeRows || a.M * scale_blocks(a.K) > kMadeBlocks || a.part || a.y_dtype == HTS_FP8_E4M3) return hipErrorInvalidValue;
+    if (a.gated) return x_dtype == HTS_BF16 ? launch_mg<true, 1, HTS_BF16>(a, s) : launch_mg<true, 1, HTS_F16>(a, s);
+    return launch_mg<false, 1, HTS_F32>(a, s);
 }
 
 hipError_t launch_scaled_sum(const ScaledArgs& a, hipStream_t s) {
