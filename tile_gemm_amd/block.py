@@ -8,8 +8,9 @@ back to back:
     q = X Wq^T,  k = X Wk^T,  v = X Wv^T,  o = A Wo^T,
     gate = X Wg^T,  up = X Wu^T,  h = silu(gate) * up,  down = h Wd^T
 
-with every W either a packed hybrid weight (hts_gemm) or a row-major dense one
-(hts_dense_gemm, the same-library baseline).  In ``forward`` the output projection reads A = q in
+with every W either a packed hybrid weight (hts_gemm), a row-major dense one
+(hts_dense_gemm, the same-library baseline) or a dense 8-bit one with a scale for each block of 128
+(ScaledWeight: its input is quantised by hts_quantize_rows and multiplied by hts_scaled_gemm).  In ``forward`` the output projection reads A = q in
 place of the attention output, which keeps the shapes and the data dependence of the block.
 Every call is enqueued on the current stream, so the whole step can be captured in one HIP
 graph.
@@ -33,8 +34,8 @@ from typing import Dict, Optional
 
 import torch
 
-from . import (HTSError, KVCache, KVStep, Norm, PackedWeight, RopePlan, dense_gemm, gemm, gemm_silu_mul, paged_attn, residual_norm,
-               rope_cache, silu_mul)
+from . import (HTSError, KVCache, KVStep, Norm, PackedWeight, RopePlan, ScaledWeight, dense_gemm, gemm, gemm_silu_mul,
+               paged_attn, quantize_rows, residual_norm, rope_cache, scaled_gated, scaled_gemm, scaled_mlp, silu_mul)
 
 PROJECTIONS = ("q", "k", "v", "o", "gate", "up", "down")
 
@@ -51,7 +52,37 @@ def buffers(M: int, weights: Dict[str, object], dtype, device) -> Dict[str, torc
 def _linear(x: torch.Tensor, w, out: torch.Tensor) -> torch.Tensor:
     if isinstance(w, PackedWeight):
         return gemm(x, w, out=out)
+    if isinstance(w, ScaledWeight):
+        return scaled_gemm(*quantize_rows(x), w, out=out)
     return dense_gemm(x, w, out=out)
+
+
+def _linears(x: torch.Tensor, names, weights: Dict[str, object], bufs: Dict[str, torch.Tensor]) -> None:
+    """Several projections of one input, quantised once for those in 8 bits."""
+    scaled = [n for n in names if isinstance(weights[n], ScaledWeight)]
+    if scaled:
+        q, scale = quantize_rows(x)
+        for n in scaled:
+            scaled_gemm(q, scale, weights[n], out=bufs[n])
+    for n in names:
+        if n not in scaled:
+            _linear(x, weights[n], bufs[n])
+
+
+def _mlp(x: torch.Tensor, w: Dict[str, object], bufs: Dict[str, torch.Tensor]) -> torch.Tensor:
+    """down(silu(gate x) * (up x)) in the fewest steps that the weights allow."""
+    scaled = [isinstance(w[n], ScaledWeight) for n in ("gate", "up", "down")]
+    if all(scaled):
+        return scaled_mlp(x, w["gate"], w["up"], w["down"], out=bufs["down"])
+    if scaled[0] and scaled[1]:
+        scaled_gated(*quantize_rows(x), w["gate"], w["up"], out=bufs["h"])
+    elif isinstance(w["up"], PackedWeight):
+        _linear(x, w["gate"], bufs["gate"])
+        gemm_silu_mul(x, w["up"], bufs["gate"], out=bufs["h"])
+    else:
+        _linears(x, ("gate", "up"), w, bufs)
+        silu_mul(bufs["gate"], bufs["up"], out=bufs["h"])
+    return _linear(bufs["h"], w["down"], bufs["down"])
 
 
 def forward(X: torch.Tensor, weights: Dict[str, object], bufs: Dict[str, torch.Tensor],
@@ -84,7 +115,7 @@ def kept_flops(M: int, weights: Dict[str, object]) -> float:
 
 @dataclasses.dataclass
 class Layer:
-    """A decoder block: its seven projections (packed or row-major), its norms and its cache.
+    """A decoder block: its seven projections (packed, row-major or in 8 bits with scales), its norms and its cache.
 
     input_norm and mlp_norm come before attention and the MLP; the optional post norms, gates ([hidden], or one
     for each token) and residual_scale apply to what the two write back to the residual stream:
@@ -103,17 +134,20 @@ class Layer:
 
     def __post_init__(self):
         # The products take any input that their leading dimension lets through: the block's own shapes are held here.
+        # 8-bit weights with scales take rows of either 16-bit type.
         shape = {n: ((w.N, w.K) if isinstance(w, PackedWeight) else tuple(w.shape), w.dtype)
                  for n, w in self.weights.items()}
         if sorted(shape) != sorted(PROJECTIONS):
             raise HTSError(1, f"a block has the projections {', '.join(PROJECTIONS)}")
-        (nq, hidden), dt = shape["q"]
+        (nq, hidden), _ = shape["q"]
         self.hidden = hidden
+        plain = [n for n in PROJECTIONS if not isinstance(self.weights[n], ScaledWeight)]
+        self.dtype = dt = shape[plain[0]][1] if plain else None      # None: the rows' own
         nk, inner = self.cache.heads * self.cache.dim, shape["gate"][0][0]
         want = dict(q=(nq, hidden), k=(nk, hidden), v=(nk, hidden), o=(hidden, nq), gate=(inner, hidden),
                     up=(inner, hidden), down=(hidden, inner))
         for n, (got, t) in shape.items():
-            if t != dt or t not in (torch.float16, torch.bfloat16):
+            if n in plain and (t != dt or t not in (torch.float16, torch.bfloat16)):
                 raise HTSError(2, f"{n} has type {t}: a block's weights share one 16-bit type")
             if got != want[n]:
                 raise HTSError(3, f"{n} is {got[0]} x {got[1]}, the block's other shapes ask for {want[n][0]} x {want[n][1]}")
@@ -140,27 +174,21 @@ def decode(x: torch.Tensor, residual: Optional[torch.Tensor], layer: Layer, step
     w, B = layer.weights, x.shape[0]
     if x.dim() != 2 or x.shape[1] != layer.hidden:
         raise HTSError(3, f"x has shape {tuple(x.shape)}, the block's hidden size is {layer.hidden}")
-    if x.dtype != w["q"].dtype:
-        raise HTSError(2, f"x has type {x.dtype}, the block's weights {w['q'].dtype}")
+    if layer.dtype is not None and x.dtype != layer.dtype:
+        raise HTSError(2, f"x has type {x.dtype}, the block's weights {layer.dtype}")
     if step.positions.numel() != B or step.lengths.numel() != B or step.starts.numel() != B + 1:
         raise HTSError(3, f"x has {B} rows, the step {step.lengths.numel()} requests and {step.positions.numel()} tokens")
     if bufs is None:
         bufs = buffers(B, w, x.dtype, x.device)
     # r = residual + x, y = norm(r)
     r, y = residual_norm(x, residual, pre=layer.input_norm)
-    for name in ("q", "k", "v"):
-        _linear(y, w[name], bufs[name])
+    _linears(y, ("q", "k", "v"), w, bufs)
     rope_cache(bufs["q"], bufs["k"], bufs["v"], step.positions, step.slots, plan, layer.cache, starts=step.starts)
     a = paged_attn(bufs["q"], layer.cache, block_table, step.lengths, layer.attn_scale, layer.window)
     _linear(a, w["o"], bufs["o"])
     r, y = residual_norm(bufs["o"], r, post=layer.post_attn_norm, pre=layer.mlp_norm, gate=layer.attn_gate,
                          scale=layer.residual_scale, residual_out=r)
-    _linear(y, w["gate"], bufs["gate"])
-    if isinstance(w["up"], PackedWeight):
-        gemm_silu_mul(y, w["up"], bufs["gate"], out=bufs["h"])
-    else:
-        silu_mul(bufs["gate"], _linear(y, w["up"], bufs["up"]), out=bufs["h"])
-    out = _linear(bufs["h"], w["down"], bufs["down"])
+    out = _mlp(y, w, bufs)
     if layer.post_mlp_norm is not None or layer.mlp_gate is not None or layer.residual_scale != 1.0:
         out, _ = residual_norm(out, None, post=layer.post_mlp_norm, gate=layer.mlp_gate, scale=layer.residual_scale)
     return out, r

@@ -19,8 +19,10 @@ extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
+// ONCE: what no other workgroup reads claims no place in the caches.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(rsrc_t r, uint32_t lds_off, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t*)((lds_u8*)smem + lds_off), 16, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t*)((lds_u8*)smem + lds_off), 16, voff, soff, 0, ONCE ? 2 : 0);
 }
 __device__ __forceinline__ void copy4(const void* g, uint32_t lds_off) {
     __builtin_amdgcn_global_load_lds(g, (lds_t*)((lds_u8*)smem + lds_off), 4, 0, 0);
@@ -50,7 +52,7 @@ struct RingShape {
     static_assert(NST >= 2 && (NST - 1) * C < 64 && TOTAL <= 160 * 1024 && NW <= 16, "ring");
 };
 
-template <bool GATED, int AB, int NB, int WN, int WM, int WK, int NST>
+template <bool GATED, bool ONCE, int AB, int NB, int WN, int WM, int WK, int NST>
 __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const ScaledArgs a, int NBK, int MBK) {
     using T = RingShape<AB, NB, WN, WM, WK, NST>;
     static_assert(!GATED || AB % 2 == 0, "gate and up");
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
         st += wk * T::BLOCK;
 #pragma unroll
         for (int v = 0; v < T::WJ; ++v)
-            copy16(GATED ? wr[wup[v]] : wr[0], st + 1024 * (wg + NG * v), wch[v] >= cols ? kOutside : wvo[v], so);
+            copy16<ONCE>(GATED ? wr[wup[v]] : wr[0], st + 1024 * (wg + NG * v), wch[v] >= cols ? kOutside : wvo[v], so);
 #pragma unroll
         for (int v = 0; v < T::XJ; ++v) copy16(xr, st + T::XOFF + 1024 * xjob[v], xch[v] >= cols ? kOutside : xvo[v], so);
         copy4(xs + (int64_t)(at < kb1 ? at : kb1 - 1) * a.ldxs, st + T::SOFF + 256 * sj);
@@ -214,10 +216,10 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
     }
 }
 
-template <bool GATED, int AB, int NB, int WN, int WM, int WK, int NST>
+template <bool GATED, bool ONCE, int AB, int NB, int WN, int WM, int WK, int NST>
 hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
     using T = RingShape<AB, NB, WN, WM, WK, NST>;
-    auto kern = scaled_ring_kernel<GATED, AB, NB, WN, WM, WK, NST>;
+    auto kern = scaled_ring_kernel<GATED, ONCE, AB, NB, WN, WM, WK, NST>;
     static DeviceOnce lds_limit;
     hipError_t e = lds_limit.run([&] {
         return hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, T::TOTAL);
@@ -229,12 +231,23 @@ hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Weights of 64 MB and more, rows of whole cache lines, and one row of workgroups for all rows of X: each line is read once, and
+// no other call finds it in the caches (24 x 32001 x 4096: 27.6 us, 31.0 without; 48 rows of two 13824 x 5120: 32.8 and 36.1.
+// On rows of 5136, whose lines two steps share, 45.2 and 43.4; 16 x 11008 x 4096 called again and again 12.8 and 11.5).
+template <int AB, int NB, int WN, int WM, int WK, int NST>
+hipError_t launch_any(const ScaledArgs& a, hipStream_t s) {
+    bool once = a.M <= 16 * NB * WM && a.N * a.K * (a.gated ? 2 : 1) >= int64_t(64) << 20;
+    for (int w = 0; w < (a.gated ? 2 : 1); ++w) once = once && a.ldw[w] % 128 == 0 && reinterpret_cast<uintptr_t>(a.W[w]) % 128 == 0;
+    if (a.gated) return once ? launch_shape<true, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<true, false, AB, NB, WN, WM, WK, NST>(a, s);
+    return once ? launch_shape<false, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<false, false, AB, NB, WN, WM, WK, NST>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_scaled_ring(const ScaledArgs& a, ScaledKernel k, hipStream_t s) {
     if (a.y_dtype == HTS_FP8_E4M3 && !a.part) return hipErrorInvalidValue;
 #define HTS_RING(name, AB, NB, WN, WM, WK, NST) \
-    if (k == name) return a.gated ? launch_shape<true, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<false, AB, NB, WN, WM, WK, NST>(a, s)
+    if (k == name) return launch_any<AB, NB, WN, WM, WK, NST>(a, s)
     HTS_RING(RING_32x16, 2, 1, 1, 1, 8, 3);
     HTS_RING(RING_64x16, 2, 1, 2, 1, 2, 4);
     HTS_RING(RING_32x32, 2, 2, 1, 1, 4, 4);

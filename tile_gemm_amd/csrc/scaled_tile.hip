@@ -45,7 +45,7 @@ struct TileShape {
     static constexpr int XOFF = BN * 128, SOFF = XOFF + BM * 128, STAGE = SOFF + BM * 4;
     static constexpr int TOTAL = 2 * STAGE;
     static constexpr int H = NBJ / 2;                     // a block's X: columns bj < H, then the others
-    static constexpr int PC = WJ + XJ / 2 + 1, QC = XJ / 2;   // copies per wave: W, X below H and scales; X from H on
+    static constexpr int XH = XJ / 2, PC = WJ + XH, QC = 1 + XH;   // copies per wave: W, X below H; scales, X from H on
     static_assert(XJ % 2 == 0 && NBJ % 4 == 0 && BM / 64 <= NW && WTM / 16 % 2 == 0, "copies");
     static_assert(WN * BM * 4 <= STAGE, "the blocks' largest values fit");
 };
@@ -86,8 +86,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     uint32_t wvo[T::WJ], xvo[T::XJ];
     // first LDS row of X copy v: rows of the columns below H come first
     auto x_row = [&](int v) {
-        const int r = 8 * (wave + NW * (v % T::QC)), half = T::WTM / 2;
-        return r / half * T::WTM + r % half + (v >= T::QC ? half : 0);
+        const int r = 8 * (wave + NW * (v % T::XH)), half = T::WTM / 2;
+        return r / half * T::WTM + r % half + (v >= T::XH ? half : 0);
     };
 #pragma unroll
     for (int v = 0; v < T::WJ; ++v) {
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     const float* xs = a.xs + m0 + (sm < rows_m ? sm : rows_m - 1);
     const int tail = (int)(a.K - (int64_t)128 * (KB - 1));            // columns of the last block
 
-    // copy c of block kb: W, X below H, the scales (0 .. PC - 1), X from H on (PC .. PC + QC - 1).  Past the last block
+    // copy c of block kb: W, X below H (0 .. PC - 1), the scales, X from H on (PC .. PC + QC - 1).  Past the last block
     // of this part the copies stay, so that as many are in flight in every step, but read zeros from outside
     // (the scales: once more the last ones).
     auto outside = [&](int kb) { return 16 * ch >= (kb >= kb1 ? 0 : kb == KB - 1 ? tail : 128); };
@@ -118,10 +118,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
         if (c < T::WJ) {
             const int job = wave + NW * c;
             copy16(wr[GATED ? (job >> 2) & 1 : 0], st + 1024 * job, cut ? kOutside : wvo[c], so);
-        } else if (c == T::PC - 1) {
+        } else if (c == T::PC) {
             copy4(xs + (int64_t)(kb < kb1 ? kb : kb1 - 1) * a.ldxs, st + T::SOFF + 256 * sj);
         } else {
-            const int v = c < T::PC ? c - T::WJ : c - T::PC + T::QC;
+            const int v = c < T::PC ? c - T::WJ : c - T::PC - 1 + T::XH;
             copy16(xr, st + T::XOFF + 128 * x_row(v), cut ? kOutside : xvo[v], so);
         }
     };
@@ -149,14 +149,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     const uint32_t sbase = T::SOFF + 4 * (wm * T::WTM + NBJ * i);
 
     // One block's sums: step t = 4 bj + b makes the piece (b, bj) and adds the scaled piece of step t - 3, whose matrix
-    // instruction has ended by then.  B of step bj + 1 is read during step bj; the next block's A, first B and scales
-    // during the last step.  Two barriers a block say what has landed and what has been read by all: one before the first
-    // read of the columns from H on, behind which the places of W, of the other columns and of the scales are free, and
-    // one before the next block's first reads.  So every copy is issued more than a block's time before it is needed.
+    // instruction has ended by then.  B of column block bj + 2 is read during bj (one ahead, the reads came too late:
+    // LDS answers after more than four matrix instructions), the next block's first two and its A during the last two.  Two
+    // barriers a block say what has landed and what has been read by all: one before the first read of the columns from H
+    // on, behind which the places of W and of the other columns are free, and one before the next block's first reads,
+    // behind which the rest is.  So every copy is issued more than a block's time before it is needed.
     auto read_a = [&](uint32_t st, int b) { return cat8(ld16(smem + st + abase + 2048 * b + c0), ld16(smem + st + abase + 2048 * b + c1)); };
     auto read_b = [&](uint32_t st, int bj) { return cat8(ld16(smem + st + bbase + 2048 * bj + c0), ld16(smem + st + bbase + 2048 * bj + c1)); };
-    u32x8 A[4], B;
-    float sx[NBJ];
+    auto read_s = [&](uint32_t st, int bj) { return *reinterpret_cast<const float*>(smem + st + sbase + 4 * bj); };
+    u32x8 A[4], B[2];
+    float sx[2];
     f32x4 p[4];
     float s0 = 0.f, s1 = 0.f;          // scales of the pieces not yet added
 #pragma unroll
@@ -169,14 +171,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int c = 0; c < T::PC + T::QC; ++c) copy(kb0 + k, c, outside(kb0 + k));
-    landed_but<T::PC + 2 * T::QC>();
+    landed_but<T::XH + T::PC + T::QC>();
     {
         const uint32_t st = (kb0 & 1) * T::STAGE;
 #pragma unroll
         for (int b = 0; b < 4; ++b) A[b] = read_a(st, b);
-        B = read_b(st, 0);
 #pragma unroll
-        for (int bj = 0; bj < NBJ; ++bj) sx[bj] = *reinterpret_cast<const float*>(smem + st + sbase + 4 * bj);
+        for (int bj = 0; bj < 2; ++bj) {
+            B[bj] = read_b(st, bj);
+            sx[bj] = read_s(st, bj);
+        }
     }
     for (int kb = kb0; kb < kb1; ++kb) {
         if (((kb - kb0) & 63) == 0) load_ws(kb);
@@ -185,42 +189,37 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
         const int l = (kb - kb0) & 63;
         const float w0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[0]), l));
         const float w1 = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[1]), l)) : w0;
-        float sxn[NBJ];
 #pragma unroll
         for (int bj = 0; bj < NBJ; ++bj) {
-            u32x8 Bn;
-            if (bj == T::H - 1) landed_but<T::PC + T::QC>();   // X from H on is in; everyone has read the rest
-            if (bj + 1 < NBJ) {
-                Bn = read_b(st, bj + 1);
-            } else {                       // the next block's W, first X and scales are in; everyone has read this block
-                landed_but<T::PC + T::QC>();
-                Bn = read_b(sn, 0);
-#pragma unroll
-                for (int c = 0; c < NBJ; ++c) sxn[c] = *reinterpret_cast<const float*>(smem + sn + sbase + 4 * c);
-            }
-            const float t0 = sx[bj] * w0, t1 = GATED ? sx[bj] * w1 : t0;
+            if (bj == T::H - 2) landed_but<T::PC + T::QC>();      // X from H on is in; everyone has read the rest
+            if (bj == NBJ - 2) landed_but<T::XH + T::PC>();       // the next block's W, first X and scales are in;
+                                                                  // everyone has read this block
+            const u32x8 Bn = bj + 2 < NBJ ? read_b(st, bj + 2) : read_b(sn, bj + 2 - NBJ);
+            const float sn2 = bj + 2 < NBJ ? read_s(st, bj + 2) : read_s(sn, bj + 2 - NBJ);
+            const float t0 = sx[0] * w0, t1 = GATED ? sx[0] * w1 : t0;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int last = bj == 0 ? NBJ - 1 : bj - 1;
-                p[b] = mfma_block(A[b], B);
+                p[b] = mfma_block(A[b], B[0]);
                 if (bj + 1 == NBJ) A[b] = read_a(sn, b);
                 // the copies of block kb + 2 go between the matrix instructions, into what has been read
-                constexpr int FIRST = T::H - 1, SLOTS = 4 * (NBJ - T::H);
+                constexpr int FIRST = T::H - 2, SLOTS = 4 * (NBJ - T::H);
                 const int slot = 4 * (bj - FIRST) + b;
                 if (slot >= 0 && slot < SLOTS)
 #pragma unroll
                     for (int c = T::PC * slot / SLOTS; c < T::PC * (slot + 1) / SLOTS; ++c) copy(kb + 2, c, cut);
-                if (bj + 1 == NBJ && b < T::QC) copy(kb + 2, T::PC + b, cut);
+                if (bj + 2 == NBJ && b < T::QC) copy(kb + 2, T::PC + b, cut);
                 if (b < 3) add(b + 1, last, (GATED && b + 1 >= 2) ? s1 : s0);
                 else add(0, bj, t0);
                 __builtin_amdgcn_sched_barrier(0);
             }
             s0 = t0;
             s1 = t1;
-            B = Bn;
+            B[0] = B[1];
+            B[1] = Bn;
+            sx[0] = sx[1];
+            sx[1] = sn2;
         }
-#pragma unroll
-        for (int bj = 0; bj < NBJ; ++bj) sx[bj] = sxn[bj];
     }
 #pragma unroll
     for (int b = 1; b < 4; ++b) add(b, NBJ - 1, (GATED && b >= 2) ? s1 : s0);

@@ -41,7 +41,7 @@ def _row_scale(t: torch.Tensor, name: str, rows: int, cols: int, dev: int) -> in
 
 
 def _new_scale(rows: int, cols: int, device) -> torch.Tensor:
-    return torch.empty((_blocks(cols), rows), dtype=torch.float32, device=device).t()
+    return torch.empty_strided((rows, _blocks(cols)), (1, rows), dtype=torch.float32, device=device)
 
 
 class ScaledWeight:
