@@ -5,6 +5,7 @@ import torch
 import tile_gemm_amd as hts
 
 import scaled_ref as ref
+from scaled_cases import GATED8, SHAPES
 from scaled_ref import DEV, E4M3, blocks
 
 pytestmark = pytest.mark.gpu
@@ -72,13 +73,6 @@ def test_weight_blocks_are_the_definition_bit_for_bit(N, K, dtype):
 # the product
 # ------------------------------------------------------------------------------------------
 
-SHAPES = [  # M, N, K: streaming, tiled; one of everything, odd sizes, short last blocks
-    (1, 1, 16), (1, 16, 128), (2, 17, 144), (5, 130, 272), (16, 64, 1024), (17, 50, 400), (32, 333, 2064), (1, 4096, 4096),
-    (33, 1, 16), (33, 65, 128), (64, 129, 144), (100, 257, 400), (129, 300, 1040), (200, 1000, 5136), (256, 256, 256),
-    (257, 513, 384), (300, 640, 16384), (520, 4100, 528),
-]
-
-
 @pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 def test_product(M, N, K, dtype):
@@ -91,7 +85,7 @@ def test_product(M, N, K, dtype):
     ref.check(y, want, bound, "product")
 
 
-@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[1] * s[2] < 3e6])
+@pytest.mark.parametrize("M,N,K", [s for s in SHAPES if s[1] * s[2] < 1.1e7])
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_gated(M, N, K, act):
     g = ref.generator(M + 3 * N + 7 * K)
@@ -104,8 +98,7 @@ def test_gated(M, N, K, act):
         ref.check(h, want, bound, act)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (7, 144, 272), (32, 4112, 400), (33, 16, 16), (64, 128, 256), (100, 272, 400),
-                                   (257, 400, 1040), (300, 1040, 528)])
+@pytest.mark.parametrize("M,N,K", GATED8)
 def test_gated_rows_in_8_bits(M, N, K):
     g = ref.generator(M + 3 * N + 7 * K)
     x, xs = ref.random_rows(g, M, K)
