@@ -135,3 +135,20 @@ def test_mlp_is_its_steps(M):
     x2 = x.clone()
     assert hts.scaled_mlp(x2, gate, up, down, act="gelu", out=x2) is x2
     assert torch.equal(x2, y)
+
+
+@pytest.mark.parametrize("M,hidden,inner", [(1, 4096, 11008), (4, 1040, 4096), (2, 528, 2064)])
+def test_the_inner_rows_of_a_few_tokens_lose_no_products(M, hidden, inner):
+    """Two launches, whose inner rows are whole 32-bit sums before they become E4M3.  With sums off by 1e-7 no value is
+    expected at E4M3's other neighbour (inner * M values, steps of 2^-4: 2^4 * 1e-7 of them), and what is left is the output's
+    half step, 2^-11, and the second product's 2^-13 of single products, 2e-5 of its norm.  Sums that drop bits move
+    ten to twenty values by an eighth of themselves: 2e-3."""
+    g = ref.generator(hidden)
+    x = torch.randn((M, hidden), generator=g, device=DEV).to(F16)
+    gate, up = (hts.ScaledWeight(*ref.random_weight(g, inner, hidden)) for _ in range(2))
+    down = hts.ScaledWeight(*ref.random_weight(g, hidden, inner))
+    y = hts.scaled_mlp(x, gate, up, down)
+    q, s = ref.quantized(x.double())
+    h, _ = ref.gated("silu", q, s, gate.values, gate.scale, up.values, up.scale)
+    want, _ = ref.product(*ref.quantized(h), down.values, down.scale)
+    assert float((y.double() - want).norm() / want.norm()) < 2.0 ** -11 + 1e-4

@@ -119,16 +119,16 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
     const int64_t tiles = (N * weights + s.rows_n - 1) / s.rows_n * mb * split;
     const int64_t steps = ((KB + split - 1) / split + s.blocks - 1) / s.blocks;
     const int at_once = k == hts::TILE_128x128 ? 512 : 256;
-    float us = 3.5f;
+    float us = 1.0f;
     const int64_t whole = tiles / at_once;
     for (int last = 0; last < 2; ++last) {
         const int64_t busy = last ? tiles % at_once : at_once, rounds = last ? (busy ? 1 : 0) : whole;
         if (!rounds) continue;
         float step = s.step;
         if (k == hts::TILE_128x128 && busy > 256) step = 1.2f;             // two on a CU
-        if (k == hts::TILE_256x256) step += 0.9f * busy / 256;             // what the matrix cores' clock and L2 leave
+        if (k == hts::TILE_256x256) step += 0.85f * busy / 256;             // what the matrix cores' clock and L2 leave
         const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / kBytesPerUs;
-        us += rounds * ((k < hts::TILE_128x128 ? 2.0f : 4.5f) + steps * std::max(step, wait));
+        us += rounds * ((k < hts::TILE_128x128 ? 4.5f : 7.0f) + steps * std::max(step, wait));
     }
     return us;
 }
@@ -225,7 +225,12 @@ MlpPlan mlp_plan(int64_t M, int64_t hidden, int64_t inner) {
     p.hs = p.hq + round256((uint64_t)M * inner);
     p.parts = p.hs + round256(4 * (uint64_t)p.lds * scale_blocks(inner));
     p.bytes = p.parts + std::max(p.gated.bytes, p.down.bytes);
-    p.made = M <= hts::kMadeRows && M * scale_blocks(hidden) <= hts::kMadeBlocks && M * scale_blocks(inner) <= hts::kMadeBlocks;
+    // Two launches save about 4.7 us of the three or four others, and lose to them with every byte of weights: their
+    // kernel streams slower, and every workgroup makes all rows.  us, two launches against the others: 4096 x 1024, four rows
+    // 11.6 : 15.1; 4096 x 4096, four rows 21.7 : 24.1; 4096 x 11008, one row 35.3 : 35.9, two rows 37.2 : 35.3; 5120 x
+    // 13824, one row 51.9 : 49.6.
+    p.made = 3.0 * hidden * inner * (0.022 + 0.01 * M) < 4.7e6 && M <= hts::kMadeRows &&
+             M * std::max(scale_blocks(hidden), scale_blocks(inner)) <= hts::kMadeBlocks;
     if (p.made) {
         p.parts = 0;
         p.bytes = round256(4 * (uint64_t)M * inner);

@@ -29,6 +29,28 @@ __device__ __forceinline__ f32x4 mfma_block(u32x8 a, u32x8 b) {
                                                             f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+// The same sum with every product whole: E4M3 values are binary16 values, and the 16-bit instructions drop nothing.
+// 7e-8 of the result's norm in place of 1.5e-5 (K = 4096), for four times the matrix instructions and the conversions.
+__device__ __forceinline__ u32x8 e4m3_halves(u32x4 q) {
+    u32x8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[i], 1.0f, false));
+        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[i], 1.0f, true));
+    }
+    return r;
+}
+__device__ __forceinline__ f32x4 mfma_block_whole(u32x8 a, u32x8 b) {
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const u32x8 x = e4m3_halves(u ? hi4(a) : lo4(a)), y = e4m3_halves(u ? hi4(b) : lo4(b));
+        c = mfma_dense<F16T>(lo4(x), lo4(y), c);
+        c = mfma_dense<F16T>(hi4(x), hi4(y), c);
+    }
+    return c;
+}
+
 // ---- rows to E4M3 ----
 
 // 16 consecutive values at column c of a row (c and K multiples of 16), as floats.

@@ -21,7 +21,10 @@ __device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) 
 
 // XT: the type of X.  HTS_FP8_E4M3: rows and scales as hts_quantize_rows makes them.  Others: every workgroup makes them
 // itself, in LDS, while its first weights are on their way.
-template <bool GATED, int KS, int NT, int MG, int XT>
+// WHOLE: no product loses bits.  For gated sums that become E4M3: an error of 1.5e-5 puts a few values of a row on E4M3's
+// other neighbour, an eighth of the value away, and one of those is seen (one token of 11008 x 4096: 4.4e-3 of the
+// result's norm against 1.7e-3, which is bfloat16's own rounding); 16-bit outputs are a hundred times coarser than it.
+template <bool GATED, int KS, int NT, int MG, int XT, bool WHOLE>
 __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs a) {
     constexpr int PP = GATED ? 2 : 1;
     constexpr bool MAKE = XT != HTS_FP8_E4M3;
@@ -79,20 +82,15 @@ __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs
             for (int p = 0; p < PP; ++p) sw[s][p] = ws[p][kb];
         }
     };
-    auto load_x = [&](int t) __attribute__((always_inline)) {
+    auto load_x = [&](int s, int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < NT; ++s) {
-            if (t + KS * s >= KB) break;
-            const int kb = t + KS * s;
+        for (int h = 0; h < MG; ++h) {
 #pragma unroll
-            for (int h = 0; h < MG; ++h) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if constexpr (MAKE) X[s][h][u] = ld16(made + xvo[h] + 128 * kb + 64 * u);
-                    else X[s][h][u] = load16(xr, kb == KB - 1 && 16 * (g + 4 * u) >= tail ? kOutside : xvo[h] + 64 * u, 128u * kb);
-                }
-                sx[s][h] = xs[h][MAKE ? kb : kb * a.ldxs];
+            for (int u = 0; u < 2; ++u) {
+                if constexpr (MAKE) X[s][h][u] = ld16(made + xvo[h] + 128 * kb + 64 * u);
+                else X[s][h][u] = load16(xr, kb == KB - 1 && 16 * (g + 4 * u) >= tail ? kOutside : xvo[h] + 64 * u, 128u * kb);
             }
+            sx[s][h] = xs[h][MAKE ? kb : kb * a.ldxs];
         }
     };
     if constexpr (MAKE) {
@@ -111,15 +109,22 @@ __global__ __launch_bounds__(64 * KS) void scaled_stream_kernel(const ScaledArgs
     }
     for (int t = wave; t < KB; t += NT * KS) {
         if (!MAKE || t != wave) load_w(t);
-        load_x(t);
+        if (!MAKE)
+#pragma unroll
+            for (int s = 0; s < NT; ++s) {
+                if (t + KS * s >= KB) break;
+                load_x(s, t + KS * s);
+            }
 #pragma unroll
         for (int s = 0; s < NT; ++s) {
             if (t + KS * s >= KB) break;
+            if (MAKE) load_x(s, t + KS * s);           // from LDS, and only then: 16 registers fewer
 #pragma unroll
             for (int h = 0; h < MG; ++h)
 #pragma unroll
                 for (int p = 0; p < PP; ++p) {
-                    const f32x4 v = mfma_block(cat8(W[s][p][0], W[s][p][1]), cat8(X[s][h][0], X[s][h][1]));
+                    const u32x8 w = cat8(W[s][p][0], W[s][p][1]), x = cat8(X[s][h][0], X[s][h][1]);
+                    const f32x4 v = WHOLE ? mfma_block_whole(w, x) : mfma_block(w, x);
                     const float sc = sx[s][h] * sw[s][p];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[h][p][e] = __builtin_fmaf(v[e], sc, acc[h][p][e]);
@@ -203,29 +208,31 @@ constexpr int kWaves = 8;
 // Four blocks of loads ahead where a wave has as many (4096 x 11008, one row: 12.1 us against 12.5 with one ahead).
 inline bool far_ahead(int64_t K) { return K > kWaves * 4 * 128; }
 
-template <bool GATED, int NT, int MG, int XT>
+template <bool GATED, int NT, int MG, int XT, bool WHOLE>
 hipError_t launch_rows(const ScaledArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), block(64 * kWaves);
     const size_t lds = XT == HTS_FP8_E4M3 ? 0 : a.M * scale_blocks(a.K) * (128 + 4);
-    scaled_stream_kernel<GATED, kWaves, NT, MG, XT><<<grid, block, lds, s>>>(a);
+    scaled_stream_kernel<GATED, kWaves, NT, MG, XT, WHOLE><<<grid, block, lds, s>>>(a);
     return hipGetLastError();
 }
-template <bool GATED, int MG, int XT = HTS_FP8_E4M3>
+template <bool GATED, int MG, int XT = HTS_FP8_E4M3, bool WHOLE = false>
 hipError_t launch_mg(const ScaledArgs& a, hipStream_t s) {
-    return far_ahead(a.K) ? launch_rows<GATED, 4, MG, XT>(a, s) : launch_rows<GATED, 1, MG, XT>(a, s);
+    return far_ahead(a.K) ? launch_rows<GATED, 4, MG, XT, WHOLE>(a, s) : launch_rows<GATED, 1, MG, XT, WHOLE>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s) {
     if (a.M > kScaledStreamRows || (a.y_dtype == HTS_FP8_E4M3 && !a.part)) return hipErrorInvalidValue;
+    constexpr int E4M3 = HTS_FP8_E4M3;
+    if (a.gated && a.part) return a.M <= 16 ? launch_mg<true, 1, E4M3, true>(a, s) : launch_mg<true, 2, E4M3, true>(a, s);
     if (a.gated) return a.M <= 16 ? launch_mg<true, 1>(a, s) : launch_mg<true, 2>(a, s);
     return a.M <= 16 ? launch_mg<false, 1>(a, s) : launch_mg<false, 2>(a, s);
 }
 
 hipError_t launch_scaled_stream_made(const ScaledArgs& a, int32_t x_dtype, hipStream_t s) {
     if (a.M > kMadeRows || a.M * scale_blocks(a.K) > kMadeBlocks || a.part || a.y_dtype == HTS_FP8_E4M3) return hipErrorInvalidValue;
-    if (a.gated) return x_dtype == HTS_BF16 ? launch_mg<true, 1, HTS_BF16>(a, s) : launch_mg<true, 1, HTS_F16>(a, s);
+    if (a.gated) return x_dtype == HTS_BF16 ? launch_mg<true, 1, HTS_BF16, true>(a, s) : launch_mg<true, 1, HTS_F16, true>(a, s);
     return launch_mg<false, 1, HTS_F32>(a, s);
 }
 
