@@ -25,6 +25,7 @@ from .serving import _16, _bad, _choice, _explain, _gpu, _lead, _scope
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _E4M3 = torch.float8_e4m3fn
 _OUT = (torch.bfloat16, torch.float16, torch.float32)
+_CODE = {t: _c._dt(t) for t in _OUT + (_E4M3,)}
 
 
 def _blocks(n: int) -> int:
@@ -116,7 +117,7 @@ def quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None, scale: Op
             out = torch.empty((M, K), dtype=_E4M3, device=x.device)
         if scale is None:
             scale = _new_scale(M, K, x.device)
-        _c._check(_c.lib().hts_quantize_rows(_c._dt(x.dtype), M, K, x.data_ptr(), ldx, out.data_ptr(), ldq,
+        _c._check(_c.lib().hts_quantize_rows(_CODE[x.dtype], M, K, x.data_ptr(), ldx, out.data_ptr(), ldq,
                                              scale.data_ptr(), lds, _c._current_stream(dev)))
     return out, scale
 
@@ -178,7 +179,7 @@ def scaled_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: ScaledWeight, out_dty
             out = _new_out(M, N, ldy, dt, w.device)
         keep, at, nbytes = _space(workspace, w._bytes((M,), lambda: _c.hts_scaled_gemm_workspace(M, N, w.K)), dev, w.device)
         _c._check(_c.lib().hts_scaled_gemm(M, N, w.K, x.data_ptr(), ldx, x_scale.data_ptr(), lds, w._desc, out.data_ptr(),
-                                           ldy, _c._dt(dt), at, nbytes, _c._current_stream(dev)))
+                                           ldy, _CODE[dt], at, nbytes, _c._current_stream(dev)))
     return out
 
 
@@ -209,7 +210,7 @@ def scaled_gated(x: torch.Tensor, x_scale: torch.Tensor, gate: ScaledWeight, up:
         keep, at, nbytes = _space(
             workspace, gate._bytes((M, dt), lambda: _c.hts_scaled_gated_workspace(M, N, K, dt)), dev, gate.device)
         _c._check(_c.lib().hts_scaled_gated(code, M, N, K, x.data_ptr(), ldx, x_scale.data_ptr(), lds, gate._desc, up._desc,
-                                            out.data_ptr(), ldh, _c._dt(dt), at_scale, ldhs, at, nbytes,
+                                            out.data_ptr(), ldh, _CODE[dt], at_scale, ldhs, at, nbytes,
                                             _c._current_stream(dev)))
     return out if out_scale is None else (out, out_scale)
 
@@ -235,6 +236,6 @@ def scaled_mlp(x: torch.Tensor, gate: ScaledWeight, up: ScaledWeight, down: Scal
             out = torch.empty((M, hidden), dtype=x.dtype, device=x.device)
         keep, at, nbytes = _space(
             workspace, gate._bytes((M, "mlp"), lambda: _c.hts_scaled_mlp_workspace(M, hidden, inner)), dev, x.device)
-        _c._check(_c.lib().hts_scaled_mlp(code, _c._DT[x.dtype], M, hidden, inner, x.data_ptr(), ldx, gate._desc, up._desc,
+        _c._check(_c.lib().hts_scaled_mlp(code, _CODE[x.dtype], M, hidden, inner, x.data_ptr(), ldx, gate._desc, up._desc,
                                           down._desc, out.data_ptr(), ldy, at, nbytes, _c._current_stream(dev)))
     return out
