@@ -105,7 +105,7 @@ constexpr Shape kShapes[hts::SCALED_KERNELS] = {
     {64, 64, 2, 0.58f},        // RING_64x64
     {128, 64, 2, 0.70f},       // RING_128x64
     {128, 128, 1, 0.60f},      // TILE_128x128
-    {256, 128, 1, 1.10f},      // TILE_256x128
+    {256, 128, 1, 0.75f},      // TILE_256x128
     {256, 256, 1, 1.05f},      // TILE_256x256
 };
 constexpr float kBytesPerUs = 6.5e6f;
@@ -126,7 +126,7 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
         if (!rounds) continue;
         float step = s.step;
         if (k == hts::TILE_128x128 && busy > 256) step = 1.2f;             // two on a CU
-        if (k == hts::TILE_256x256) step += 0.85f * busy / 256;             // what the matrix cores' clock and L2 leave
+        if (k >= hts::TILE_256x128) step += (k == hts::TILE_256x256 ? 0.85f : 0.3f) * busy / 256;   // what clock and L2 leave
         const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / kBytesPerUs;
         us += rounds * ((k < hts::TILE_128x128 ? 4.5f : 7.0f) + steps * std::max(step, wait));
     }

@@ -38,6 +38,35 @@ __device__ __forceinline__ void landed_but() {
     asm volatile("" ::: "memory");
 }
 
+// The tile of outputs of ES bytes as it lies in LDS on its way out: BM rows of BNO, their 16-byte chunks XORed with the lane
+// group that writes them, so that 16 rows written at once (NBJ apart) lie in 16 different chunks.
+template <int BNO, int NBJ, int ES>
+__device__ __forceinline__ uint32_t image_at(int row, int byte) {
+    constexpr int PITCH = BNO * ES, CHUNKS = PITCH / 16;
+    return (uint32_t)(row * PITCH + (((byte >> 4) ^ (row / NBJ % 16 % CHUNKS)) << 4) + (byte & 15));
+}
+// From there to memory, 16 bytes a lane, a row's lanes next to one another (rows of Y are 8 bytes aligned at least).
+template <int BNO, int BM, int NBJ, int ES, int THREADS>
+__device__ __forceinline__ void store_image(uint8_t* Y, int64_t ldy, int64_t rows, int64_t cols) {
+    typedef u32x4 u32x4_of_8 __attribute__((aligned(8)));
+    constexpr int CHUNKS = BNO * ES / 16, PER = 16 / ES;
+#pragma unroll
+    for (int it = 0; it < BM * CHUNKS / THREADS; ++it) {
+        const int id = it * THREADS + threadIdx.x, row = id / CHUNKS, c = id % CHUNKS;
+        const int64_t left = cols - c * PER;
+        if (row >= rows || left <= 0) continue;
+        const u32x4 v = ld16(smem + image_at<BNO, NBJ, ES>(row, 16 * c));
+        uint8_t* to = Y + (row * ldy + c * PER) * ES;
+        if (left >= PER) {
+            *reinterpret_cast<u32x4_of_8*>(to) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)                    // (E4M3 rows end with whole chunks)
+                if (e < left) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+        }
+    }
+}
+
 template <int WN, int WM, int BM>
 struct TileShape {
     static constexpr int NW = WN * WM, BN = 64 * WN, WTM = BM / WM, NBJ = WTM / 16;
@@ -252,7 +281,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
                 }
         if constexpr (BNO == 128) {
             if (a.y_dtype == HTS_FP8_E4M3) {
-                float* tops = reinterpret_cast<float*>(smem);
+                static_assert(BM * BNO + WN * BM * 4 <= T::TOTAL, "the rows and their largest values fit");
+                float* tops = reinterpret_cast<float*>(smem + BM * BNO);
                 float t[NBJ];
 #pragma unroll
                 for (int bj = 0; bj < NBJ; ++bj) {
@@ -266,7 +296,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
                     if (g == 0) tops[wn * BM + wm * T::WTM + NBJ * i + bj] = t[bj];
                 }
                 __syncthreads();
-                uint8_t* Y = static_cast<uint8_t*>(a.Y);
 #pragma unroll
                 for (int bj = 0; bj < NBJ; ++bj) {
                     const int at = wm * T::WTM + NBJ * i + bj;
@@ -274,20 +303,33 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
 #pragma unroll
                     for (int w = 0; w < WN; ++w) top = fmaxf(top, tops[w * BM + at]);
                     const float r = kE4m3Max / top;
-                    if (m1 + bj >= a.M) continue;
-                    if (wn == 0 && g == 0) a.ys[nb * a.ldys + m1 + bj] = top / kE4m3Max;
+                    if (wn == 0 && g == 0 && m1 + bj < a.M) a.ys[nb * a.ldys + m1 + bj] = top / kE4m3Max;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const int64_t n = nr + 16 * b + 4 * g;
                         float f[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) f[e] = acc[b][bj][e] * r;
-                        if (n < a.N) *reinterpret_cast<uint32_t*>(Y + (m1 + bj) * a.ldy + n) = narrow4_e4m3(f);
+                        *reinterpret_cast<uint32_t*>(smem + image_at<BNO, NBJ, 1>(at, (int)(nr - n0) + 16 * b + 4 * g)) =
+                            narrow4_e4m3(f);
                     }
                 }
+                __syncthreads();
+                store_image<BNO, BM, NBJ, 1, 64 * T::NW>(static_cast<uint8_t*>(a.Y) + m0 * a.ldy + n0, a.ldy, a.M - m0, a.N - n0);
                 return;
             }
         }
+    }
+    if (a.y_dtype != HTS_F32) {
+        static_assert(BM * BNO * 2 <= T::TOTAL, "the outputs fit");
+#pragma unroll
+        for (int b = 0; b < (GATED ? 2 : 4); ++b)
+#pragma unroll
+            for (int bj = 0; bj < NBJ; ++bj)
+                store_y4(smem + image_at<BNO, NBJ, 2>(wm * T::WTM + NBJ * i + bj, 2 * ((int)(nr - n0) + 16 * b + 4 * g)), 0,
+                         a.y_dtype, acc[b][bj]);
+        __syncthreads();
+        store_image<BNO, BM, NBJ, 2, 64 * T::NW>(static_cast<uint8_t*>(a.Y) + 2 * (m0 * a.ldy + n0), a.ldy, a.M - m0, a.N - n0);
+        return;
     }
 #pragma unroll
     for (int b = 0; b < (GATED ? 2 : 4); ++b) {
