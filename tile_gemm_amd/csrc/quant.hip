@@ -10,12 +10,16 @@
 namespace hts {
 namespace {
 
-// Eight lanes to a block of a row, 16 values each; a workgroup's 32 blocks run along the row.
+// Eight lanes to a block of a row, 16 values each.  A workgroup takes 8 rows by 4 blocks: 1 KB of a 16-bit row in one piece,
+// and 8 scales, which lie together, in one (4-byte writes on their own cost 32 bytes of traffic each).  Bound by memory:
+// 16384 x 13824 bfloat16 in 124.6 us, 686 MB at 5.5 TB/s (a copy of 2 GiB: 4.9 TB/s).  32 blocks along a row in place of
+// 8 x 4 (us): 16384 x 13824 125.1 : 124.6, 16384 x 4096 40.8 : 37.7, 2048 x 4096 7.4 : 6.9, 1 x 4096 2.4 : 2.6.
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantArgs a, int64_t KB) {
-    const int64_t id = (blockIdx.y * kGridX + blockIdx.x) * 32 + (threadIdx.x >> 3);
-    const int64_t m = id / KB, kb = id % KB;
-    if (m >= a.M) return;
+    const int64_t id = blockIdx.y * kGridX + blockIdx.x, K4 = (KB + 3) / 4;
+    const int b = threadIdx.x >> 3;
+    const int64_t m = id / K4 * 8 + (b >> 2), kb = id % K4 * 4 + (b & 3);
+    if (m >= a.M || kb >= KB) return;
     const int64_t c = kb * kScaleBlock + 16 * (threadIdx.x & 7);
     const bool in = c < a.K;
     float f[16] = {};
@@ -62,7 +66,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(const QuantArgs a,
 
 hipError_t launch_quantize_rows(const QuantArgs& a, hipStream_t s) {
     const int64_t KB = scale_blocks(a.K);
-    const WideGrid wide = wide_grid((a.M * KB + 31) / 32);
+    const WideGrid wide = wide_grid((a.M + 7) / 8 * ((KB + 3) / 4));
     const dim3 grid(wide.x, wide.rest), block(256);
     if (a.dtype == HTS_F32) quantize_rows_kernel<HTS_F32><<<grid, block, 0, s>>>(a, KB);
     else if (a.dtype == HTS_BF16) quantize_rows_kernel<HTS_BF16><<<grid, block, 0, s>>>(a, KB);
