@@ -71,7 +71,7 @@ hipError_t launch_scaled_stream_made(const ScaledArgs& a, int32_t x_dtype, hipSt
     return hipSuccess;
 }
 hipError_t launch_scaled_ring(const ScaledArgs& a, ScaledKernel k, hipStream_t) {
-    look(a, k, k <= RING_32x16 || k == RING_32x32 ? 32 : k == RING_128x64 ? 128 : 64, 16, 512);
+    look(a, k, k <= RING_32x16 || k == RING_32x32 ? 32 : k == RING_128x64 || k == RING_128x128 ? 128 : 64, 16, 512);
     return hipSuccess;
 }
 hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledKernel k, hipStream_t) {

@@ -58,7 +58,7 @@ def test_scaled_entry_points_are_clean_under_asan_and_ubsan(driver):
 
 
 def test_the_gpu_tests_reach_every_kernel(driver):
-    names = ["stream", "ring 32x16", "ring 64x16", "ring 32x32", "ring 64x32", "ring 64x64", "ring 128x64",
+    names = ["stream", "ring 32x16", "ring 64x16", "ring 32x32", "ring 64x32", "ring 64x64", "ring 128x64", "ring 128x128",
              "tile 128x128", "tile 256x128", "tile 256x256"]
     for gated, out8, shapes in ((0, 0, SHAPES), (1, 0, SHAPES), (1, 1, GATED8)):
         args = [v for s in shapes for v in (*s, gated, out8)]

@@ -89,7 +89,7 @@ struct Plan {
 };
 
 // The kernel and split with the least estimated time.  A kernel's step (`blocks` of K on rows_n x rows_m) takes `step` us
-// with one workgroup on each of some CUs, and no less than its weights take from memory at 6.5 TB/s; workgroups beyond a
+// with one workgroup on each of some CUs, and no less than its weights take from memory; workgroups beyond a
 // CU's each (two: TILE_128x128) wait for another round.  Measured steps, and the kernels against one another (us, in
 // the order of their rows of X): the table in the comment of each kernel file.
 struct Shape {
@@ -103,12 +103,12 @@ constexpr Shape kShapes[hts::SCALED_KERNELS] = {
     {32, 32, 4, 0.42f},        // RING_32x32
     {64, 32, 2, 0.31f},        // RING_64x32
     {64, 64, 2, 0.58f},        // RING_64x64
-    {128, 64, 2, 0.70f},       // RING_128x64
+    {128, 64, 2, 0.92f},       // RING_128x64
+    {128, 128, 1, 0.68f},      // RING_128x128
     {128, 128, 1, 0.60f},      // TILE_128x128
     {256, 128, 1, 0.75f},      // TILE_256x128
     {256, 256, 1, 1.05f},      // TILE_256x256
 };
-constexpr float kBytesPerUs = 6.5e6f;
 
 float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weights, int split) {
     if (k == hts::SCALED_STREAM)
@@ -127,7 +127,9 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
         float step = s.step;
         if (k == hts::TILE_128x128 && busy > 256) step = 1.2f;             // two on a CU
         if (k >= hts::TILE_256x128) step += (k == hts::TILE_256x256 ? 0.85f : 0.3f) * busy / 256;   // what clock and L2 leave
-        const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / kBytesPerUs;
+        if (k == hts::RING_128x128) step += 0.17f * busy / 256;
+        const float bytes_per_us = k < hts::TILE_128x128 ? 6.5e6f : 4.0e6f;     // the tiles' two stages hold fewer in flight
+        const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / bytes_per_us;
         us += rounds * ((k < hts::TILE_128x128 ? 4.5f : 7.0f) + steps * std::max(step, wait));
     }
     return us;
@@ -168,7 +170,7 @@ hts_status run(hts::ScaledArgs& a, const Plan& p, void* workspace, size_t worksp
         a.nsplit = 1;
     }
     hipError_t e = p.kernel == hts::SCALED_STREAM     ? hts::launch_scaled_stream(a, s)
-                   : p.kernel <= hts::RING_128x64 ? hts::launch_scaled_ring(a, p.kernel, s)
+                   : p.kernel <= hts::RING_128x128 ? hts::launch_scaled_ring(a, p.kernel, s)
                                                   : hts::launch_scaled_tile(a, p.kernel, s);
     if (e == hipSuccess && a.part) e = hts::launch_scaled_sum(a, s);
     return hip_status(e, "scaled product kernel launch");

@@ -57,7 +57,7 @@ struct ScaledArgs {
 constexpr int64_t kScaledStreamRows = 32;
 enum ScaledKernel {
     SCALED_STREAM = 0,
-    RING_32x16, RING_64x16, RING_32x32, RING_64x32, RING_64x64, RING_128x64,
+    RING_32x16, RING_64x16, RING_32x32, RING_64x32, RING_64x64, RING_128x64, RING_128x128,
     TILE_128x128, TILE_256x128, TILE_256x256,
     SCALED_KERNELS
 };

@@ -59,7 +59,10 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
     constexpr int NG = T::NG, BNO = GATED ? T::BN / 2 : T::BN, RW = GATED ? 8 * AB : 16 * AB, HB = GATED ? AB / 2 : AB;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave / NG, wg = wave % NG, wn = wg % WN, wm = wg / WN;
-    const int nb = blockIdx.x % NBK, mb = blockIdx.x / NBK;
+    // each XCD (id % 8) takes a contiguous range, the workgroups of the same rows of W next to one another: its L2 serves them
+    int id = blockIdx.x;
+    if (MBK > 1 && id < NBK * MBK / 8 * 8) id = id % 8 * (NBK * MBK / 8) + id / 8;
+    const int nb = id / MBK, mb = id % MBK;
     const int64_t n0 = (int64_t)nb * BNO, m0 = (int64_t)mb * T::BM;
     const int KB = (int)((a.K + 127) / 128);
     const int split = blockIdx.y;
@@ -254,6 +257,7 @@ hipError_t launch_scaled_ring(const ScaledArgs& a, ScaledKernel k, hipStream_t s
     HTS_RING(RING_64x32, 2, 2, 2, 1, 2, 4);
     HTS_RING(RING_64x64, 2, 4, 2, 1, 2, 4);
     HTS_RING(RING_128x64, 2, 4, 4, 1, 2, 3);
+    HTS_RING(RING_128x128, 2, 4, 4, 2, 1, 4);
 #undef HTS_RING
     return hipErrorInvalidValue;
 }
