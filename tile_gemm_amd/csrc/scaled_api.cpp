@@ -89,9 +89,19 @@ struct Plan {
 };
 
 // The kernel and split with the least estimated time.  A kernel's step (`blocks` of K on rows_n x rows_m) takes `step` us
-// with one workgroup on each of some CUs, and no less than its weights take from memory; workgroups beyond a
-// CU's each (two: TILE_128x128) wait for another round.  Measured steps, and the kernels against one another (us, in
-// the order of their rows of X): the table in the comment of each kernel file.
+// with one workgroup on each of some CUs, and no less than its weights take from memory; workgroups beyond a CU's each (two:
+// TILE_128x128) wait for another round, and a round costs its start and end.  The steps are fitted to every kernel and
+// split timed at 60 sizes; over them the choice takes 1.01 to 1.07 of the best one's time (geometric means).  Both sides of
+// the choices that users meet most (us):
+//   1 x 11008 x 4096 gated          stream 19.1, ring 128x64 20.2      8 rows          stream 20.4, ring 128x64 20.3
+//   32 x 11008 x 4096 gated         ring 128x64 21.7, stream 27.3      16 x 11008 x 4096   ring 64x16 11.3, 64x32 11.8
+//   48 x 13824 x 5120 gated         ring 128x64 33.3, 128x128 36.4     100 rows        ring 128x128 39.9, tile 128x128 45.4
+//   64 x 11008 x 4096               ring 64x64 15.5, 128x64 17.2       32 x 4096 x 11008   ring 32x16 13.0, in two 15.0
+//   128 x 11008 x 4096              ring 128x64 18.0, tile 128x128 in two 22.0
+//   256 x 11008 x 4096              tile 128x128 24.5, ring 128x128 28.9
+//   333 x 5504 x 4144 gated         tile 256x128 43.0, 128x128 45.8    512 x 11008 x 4096  256x256 64.5, 128x128 67.2
+//   2048 x 4096 x 11008             tile 256x128 91.5, 128x128 95, 256x256 120
+//   8192 x 13824 x 5120             tile 256x256 497, 128x128 578, 256x128 586
 struct Shape {
     int rows_n, rows_m, blocks;
     float step;
@@ -130,7 +140,7 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
         if (k == hts::RING_128x128) step += 0.17f * busy / 256;
         const float bytes_per_us = k < hts::TILE_128x128 ? 6.5e6f : 4.0e6f;     // the tiles' two stages hold fewer in flight
         const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / bytes_per_us;
-        us += rounds * ((k < hts::TILE_128x128 ? 4.5f : 7.0f) + steps * std::max(step, wait));
+        us += rounds * ((k < hts::RING_128x128 ? 4.5f : k < hts::TILE_128x128 ? 6.0f : 7.0f) + steps * std::max(step, wait));
     }
     return us;
 }

@@ -5,6 +5,14 @@
 // of its W rows from the gate, half from up) and copies blocks of 128 columns into a ring of NST stages, NST - 1 ahead;
 // one barrier a block says that the next one has landed and the last one has been read.  Each wave makes AB x NB pieces
 // of 16 x 16 with one 16x16x128 instruction each, multiplies them by both scales and adds them in 32 bits.
+//
+// Bound by the weights' bytes as long as one row of workgroups covers X: 24 x 32001 x 4096, 131 MB, 24.4 us, 5.4 TB/s; 48 rows of
+// two 13824 x 5120, 142 MB, 32.5 us, 4.4 TB/s, each byte fetched once (measured).  With more rows it is the step itself, 0.9
+// us for 48 KB of copies, LDS reads and products that only partly overlap: 200 x 5000 x 5136, 26 MB, 20.4 us, the matrix cores
+// busy 10%.  Rows that are no whole number of cache lines apart cost about a sixth (gated 333 x 5504: K = 4096 36.6 us, 4144 43.0).
+// Measured against this form (us): two kernels back to back in place of the ring, 24 x 32001 x 4096 54.9 and 48 rows of two
+// 13824 x 5120 82; operands read a step ahead, no difference; products whole in 16 bits (mfma_block_whole), 64 x 11008 x 4096
+// gated 27.1 to 31.2.
 #include "scaled_device.h"
 
 namespace hts {
@@ -60,6 +68,8 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wk = wave / NG, wg = wave % NG, wn = wg % WN, wm = wg / WN;
     // each XCD (id % 8) takes a contiguous range, the workgroups of the same rows of W next to one another: its L2 serves them
+    // (us, against W's rows one after another: 128 x 13824 x 5120 26.7 to 21.9, gated 1000 x 704 x 4096 19.8 to 17.5; 512 x
+    // 2048 x 2048, where all lies in the caches, 9.6 to 10.1)
     int id = blockIdx.x;
     if (MBK > 1 && id < NBK * MBK / 8 * 8) id = id % 8 * (NBK * MBK / 8) + id / 8;
     const int nb = id / MBK, mb = id % MBK;

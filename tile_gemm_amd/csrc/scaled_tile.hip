@@ -5,6 +5,15 @@
 // A workgroup owns 64 WN rows of W and BM rows of X (the gated form: 32 WN gate rows and the same up rows), and walks K
 // in its blocks of 128.  One 16x16x128 instruction makes a 16 x 16 piece of a block's sum; the piece is multiplied by
 // both scales and added to its 32-bit accumulator on the vector units, while the matrix cores make the next ones.
+//
+// 8192 x 13824 x 5120: 497 to 526 us with the box, 2.2 to 2.3 PFLOP/s; the library's product of the same values without
+// scales takes 434, one of 8192 cubed reaches 2.86 PFLOP/s.  Bound by what a block's 2048 cycles of matrix instructions do not
+// hide: 3700 to 3900 pass a block (256 x 256), the matrix cores are busy 55%, the vector units, which add the pieces, 48%;
+// returns of LDS reads stand in the way of the matrix instructions, and the clock falls to 1.95 GHz.  Steps that made it
+// (us): one tile shape, copies a block ahead 642; pieces added three steps behind their instruction, copies between
+// the instructions 568; operands two column blocks ahead 561; outputs through LDS in whole lines 543 to 491, 3000 x 20000 x
+// 1024 114 to 85 (32 bytes of a line at a time wrote 368 MB for 226).  Measured and dropped: W from memory straight into
+// registers (256 x 192: 918 for 568), lines touched ahead, the order of K turned per workgroup (563 to 607 for 571).
 #include "scaled_device.h"
 
 namespace hts {
