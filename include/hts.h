@@ -503,8 +503,8 @@ hts_status hts_quantize_weight(int32_t dtype, int64_t N, int64_t K, const void* 
  * power of two; the scaled sums are added in 32 bits and rounded once.  For values spread as a quantised normal
  * distribution that is an error of 1.5e-5 in the 2-norm, also of an HTS_F32 output.  The product of the two scales
  * is 32-bit too.  A NaN value, or a NaN or infinite scale, makes its row or column of Y NaN or infinite.
- * Rows past M are not read.  M == 0 is a no-op.  workspace: hts_scaled_gemm_workspace() bytes, 16-byte aligned, or NULL:
- * with less the product runs unsplit, with another order of its 32-bit sums.  Results are deterministic for a given
+ * Rows past M are not read, and Y must not overlap what is read.  M == 0 is a no-op.  workspace:
+ * hts_scaled_gemm_workspace() bytes, 16-byte aligned, or NULL: with less the product runs unsplit, with another order of its 32-bit sums.  Results are deterministic for a given
  * shape and workspace.  Calls that share a workspace must not overlap. */
 hts_status hts_scaled_gemm(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* x_scale,
                            int64_t ldxs, const hts_scaled_weight* W, void* Y, int64_t ldy, int32_t y_dtype,
@@ -519,6 +519,8 @@ enum { HTS_ACT_SILU = 0, HTS_ACT_GELU = 1, HTS_ACT_GELU_TANH = 2 };
  *   h_dtype HTS_F32, HTS_F16, HTS_BF16 : h_scale must be NULL; ldh >= N a multiple of 4, any N
  *   h_dtype HTS_FP8_E4M3               : H rows of values and h_scale [ceil(N/128), ldhs] as hts_quantize_rows makes
  *                                        them of the unrounded H; N and ldh multiples of 16.  The next product's X.
+ *                                        An error of 1.5e-5 in H puts a few values in ten thousand on E4M3's other
+ *                                        neighbour (hts_scaled_mlp in HTS_BF16: 2.4e-3 of Y's 2-norm, 1.7e-3 without).
  * workspace: hts_scaled_gated_workspace() bytes; optional, but for HTS_FP8_E4M3, which may need all of them
  * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm. */
 hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
