@@ -6,7 +6,7 @@
 // in its blocks of 128.  One 16x16x128 instruction makes a 16 x 16 piece of a block's sum; the piece is multiplied by
 // both scales and added to its 32-bit accumulator on the vector units, while the matrix cores make the next ones.
 //
-// 8192 x 13824 x 5120: 497 to 526 us with the box, 2.2 to 2.3 PFLOP/s; the library's product of the same values without
+// 8192 x 13824 x 5120: 497 to 526 us from card to card, 2.2 to 2.3 PFLOP/s; the library's product of the same values without
 // scales takes 434, one of 8192 cubed reaches 2.86 PFLOP/s.  Bound by what a block's 2048 cycles of matrix instructions do not
 // hide: 3700 to 3900 pass a block (256 x 256), the matrix cores are busy 55%, the vector units, which add the pieces, 48%;
 // returns of LDS reads stand in the way of the matrix instructions, and the clock falls to 1.95 GHz.  Steps that made it
