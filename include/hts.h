@@ -519,8 +519,8 @@ enum { HTS_ACT_SILU = 0, HTS_ACT_GELU = 1, HTS_ACT_GELU_TANH = 2 };
  *   h_dtype HTS_F32, HTS_F16, HTS_BF16 : h_scale must be NULL; ldh >= N a multiple of 4, any N
  *   h_dtype HTS_FP8_E4M3               : H rows of values and h_scale [ceil(N/128), ldhs] as hts_quantize_rows makes
  *                                        them of the unrounded H; N and ldh multiples of 16.  The next product's X.
- *                                        An error of 1.5e-5 in H puts a few values in ten thousand on E4M3's other
- *                                        neighbour (hts_scaled_mlp in HTS_BF16: 2.4e-3 of Y's 2-norm, 1.7e-3 without).
+ *                                        The sums behind them lose no products: a value is its definition's E4M3
+ *                                        neighbour unless it lies nearer to a tie than a 32-bit sum is exact.
  * workspace: hts_scaled_gated_workspace() bytes; optional, but for HTS_FP8_E4M3, which may need all of them
  * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm. */
 hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,

@@ -102,25 +102,30 @@ struct Plan {
 //   333 x 5504 x 4144 gated         tile 256x128 43.0, 128x128 45.8    512 x 11008 x 4096  256x256 64.5, 128x128 67.2
 //   2048 x 4096 x 11008             tile 256x128 91.5, 128x128 95, 256x256 120
 //   8192 x 13824 x 5120             tile 256x256 497, 128x128 578, 256x128 586
+// Whole sums (`whole` us a step), gated to E4M3 rows, the second launch of those that leave parts included:
+//   1 x 11008 x 4096                stream 24.5, ring 64x16 25.4       4 x 13824 x 5120    ring 64x16 31.0, 64x32 33.6
+//   64 x 11008 x 4096               ring 128x64 31.2, in two 37.4      100 rows        tile 128x128 in two 44.4, in one 44.7
+//   200 x 11008 x 4096              tile 256x128 61.4, 128x128 in two 65.5     512 rows    128x128 109, 256x128 120
+//   2048 x 11008 x 4096             tile 256x128 359, 128x128 371
 struct Shape {
     int rows_n, rows_m, blocks;
-    float step;
+    float step, whole;
 };
 constexpr Shape kShapes[hts::SCALED_KERNELS] = {
-    {16, 32, 8, 0.0f},         // SCALED_STREAM (its own estimate)
-    {32, 16, 8, 0.55f},        // RING_32x16
-    {64, 16, 2, 0.22f},        // RING_64x16
-    {32, 32, 4, 0.42f},        // RING_32x32
-    {64, 32, 2, 0.31f},        // RING_64x32
-    {64, 64, 2, 0.58f},        // RING_64x64
-    {128, 64, 2, 0.92f},       // RING_128x64
-    {128, 128, 1, 0.68f},      // RING_128x128
-    {128, 128, 1, 0.60f},      // TILE_128x128
-    {256, 128, 1, 0.75f},      // TILE_256x128
-    {256, 256, 1, 1.05f},      // TILE_256x256
+    {16, 32, 8, 0.0f, 0.0f},          // SCALED_STREAM (its own estimate)
+    {32, 16, 8, 0.55f, 0.68f},        // RING_32x16
+    {64, 16, 2, 0.22f, 0.38f},        // RING_64x16
+    {32, 32, 4, 0.42f, 0.53f},        // RING_32x32
+    {64, 32, 2, 0.31f, 0.50f},        // RING_64x32
+    {64, 64, 2, 0.58f, 0.78f},        // RING_64x64
+    {128, 64, 2, 0.92f, 1.22f},       // RING_128x64
+    {128, 128, 1, 0.68f, 1.00f},      // RING_128x128
+    {128, 128, 1, 0.60f, 1.02f},      // TILE_128x128
+    {256, 128, 1, 0.75f, 1.60f},      // TILE_256x128
+    {256, 256, 1, 1.05f, 0.0f},       // TILE_256x256 (no whole sums)
 };
 
-float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weights, int split) {
+float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weights, int split, bool whole) {
     if (k == hts::SCALED_STREAM)
         return 4.0f + std::max(weights * (float)N * KB * 128 / 5.5e6f * (1.0f + M / 40.0f),
                                0.35f * (weights + (M + 15) / 16) * ((KB + 7) / 8));     // a wave's loads, one block at a time
@@ -130,22 +135,24 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
     const int64_t steps = ((KB + split - 1) / split + s.blocks - 1) / s.blocks;
     const int at_once = k == hts::TILE_128x128 ? 512 : 256;
     float us = 1.0f;
-    const int64_t whole = tiles / at_once;
+    const int64_t full = tiles / at_once;
     for (int last = 0; last < 2; ++last) {
-        const int64_t busy = last ? tiles % at_once : at_once, rounds = last ? (busy ? 1 : 0) : whole;
+        const int64_t busy = last ? tiles % at_once : at_once, rounds = last ? (busy ? 1 : 0) : full;
         if (!rounds) continue;
-        float step = s.step;
-        if (k == hts::TILE_128x128 && busy > 256) step = 1.2f;             // two on a CU
+        float step = whole ? s.whole : s.step;
+        if (k == hts::TILE_128x128 && busy > 256) step = whole ? 1.8f : 1.2f;             // two on a CU
         if (k >= hts::TILE_256x128) step += (k == hts::TILE_256x256 ? 0.85f : 0.3f) * busy / 256;   // what clock and L2 leave
         if (k == hts::RING_128x128) step += 0.17f * busy / 256;
-        const float bytes_per_us = k < hts::TILE_128x128 ? 6.5e6f : 4.0e6f;     // the tiles' two stages hold fewer in flight
+        // the tiles' two stages hold fewer bytes in flight, and so do three where whole sums make a step longer
+        const float bytes_per_us = k >= hts::TILE_128x128 ? 4.0e6f : whole && k == hts::RING_128x64 ? 5.2e6f : 6.5e6f;
         const float wait = (float)busy / std::min(mb, busy) * s.rows_n * s.blocks * 128 / bytes_per_us;
         us += rounds * ((k < hts::RING_128x128 ? 4.5f : k < hts::TILE_128x128 ? 6.0f : 7.0f) + steps * std::max(step, wait));
     }
     return us;
 }
 
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool out8) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int32_t y_dtype) {
+    const bool out8 = y_dtype == HTS_FP8_E4M3, whole = hts::whole_sums(y_dtype);
     Plan p{};
     p.ldp = (N + 3) / 4 * 4;
     const int64_t KB = scale_blocks(K);
@@ -154,11 +161,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, bool out8) {
     float best = 0.0f;
     for (int i = 0; i < hts::SCALED_KERNELS; ++i) {
         const auto k = (hts::ScaledKernel)i;
-        if (k == hts::SCALED_STREAM && M > hts::kScaledStreamRows) continue;
+        if ((k == hts::SCALED_STREAM && M > hts::kScaledStreamRows) || (k == hts::TILE_256x256 && whole)) continue;
         for (int split = 1; split <= 8; split *= 2) {
             if (split > KB || (split > 1 && k == hts::SCALED_STREAM)) break;
             const bool parts = split > 1 || (out8 && !hts::writes_e4m3(k));
-            const float us = estimate(k, M, N, KB, weights, split) + (parts ? 3.0f + split * plane : 0.0f);
+            const float us = estimate(k, M, N, KB, weights, split, whole) + (parts ? 3.0f + split * plane : 0.0f);
             if (!p.nsplit || us < best) {
                 best = us;
                 p.kernel = k;
@@ -229,8 +236,8 @@ struct MlpPlan {
 };
 MlpPlan mlp_plan(int64_t M, int64_t hidden, int64_t inner) {
     MlpPlan p{};
-    p.gated = plan_of(M, inner, hidden, true, true);
-    p.down = plan_of(M, hidden, inner, false, false);
+    p.gated = plan_of(M, inner, hidden, true, HTS_FP8_E4M3);
+    p.down = plan_of(M, hidden, inner, false, HTS_BF16);
     p.lds = (M + 3) / 4 * 4;
     p.xs = round256((uint64_t)M * hidden);
     p.hq = p.xs + round256(4 * (uint64_t)p.lds * scale_blocks(hidden));
@@ -287,14 +294,14 @@ hts_status hts_scaled_gemm(int64_t M, int64_t N, int64_t K, const void* X, int64
     a.Y = Y;
     a.ldy = ldy;
     a.y_dtype = y_dtype;
-    return run(a, plan_of(M, N, K, false, false), workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+    return run(a, plan_of(M, N, K, false, y_dtype), workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 hts_status hts_scaled_gemm_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes) {
     hts_status st = check_shape(M, N, K);
     if (st) return st;
     if (!bytes) return fail(HTS_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = (size_t)plan_of(M, N, K, false, false).bytes;
+    *bytes = (size_t)plan_of(M, N, K, false, HTS_BF16).bytes;
     return ok();
 }
 
@@ -315,7 +322,7 @@ hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const 
     if (out8 && (st = check_scale(h_scale, ldhs, M, "h_scale"))) return st;
     if (!out8 && h_scale) return fail(HTS_ERR_INVALID_ARG, "h_scale belongs to an E4M3 output");
     if (workspace && !aligned16(workspace)) return fail(HTS_ERR_ALIGN, "workspace is not 16-byte aligned");
-    const Plan p = plan_of(M, N, K, true, out8);
+    const Plan p = plan_of(M, N, K, true, h_dtype);
     if (p.need && (!workspace || workspace_bytes < p.bytes))
         return fail(HTS_ERR_WORKSPACE, "workspace of %zu bytes, hts_scaled_gated_workspace asks for %llu",
                     workspace ? workspace_bytes : (size_t)0, (unsigned long long)p.bytes);
@@ -346,7 +353,7 @@ hts_status hts_scaled_gated_workspace(int64_t M, int64_t N, int64_t K, int32_t h
     hts_status st = check_shape(M, N, K);
     if (st) return st;
     if (!bytes) return fail(HTS_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = (size_t)plan_of(M, N, K, true, h_dtype == HTS_FP8_E4M3).bytes;
+    *bytes = (size_t)plan_of(M, N, K, true, h_dtype).bytes;
     return ok();
 }
 

@@ -30,7 +30,7 @@ __device__ __forceinline__ f32x4 mfma_block(u32x8 a, u32x8 b) {
 }
 
 // The same sum with every product whole: E4M3 values are binary16 values, and the 16-bit instructions drop nothing.
-// 7e-8 of the result's norm in place of 1.5e-5 (K = 4096), for four times the matrix instructions and the conversions.
+// 7e-8 of the result's norm in place of 1.5e-5 (K = 4096), for twice the matrix cores' time and the conversions.
 __device__ __forceinline__ u32x8 e4m3_halves(u32x4 q) {
     u32x8 r;
 #pragma unroll
@@ -40,15 +40,20 @@ __device__ __forceinline__ u32x8 e4m3_halves(u32x4 q) {
     }
     return r;
 }
-__device__ __forceinline__ f32x4 mfma_block_whole(u32x8 a, u32x8 b) {
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+struct Halves {
+    u32x8 v[2];
+};
+__device__ __forceinline__ Halves e4m3_halves(u32x8 q) { return {{e4m3_halves(lo4(q)), e4m3_halves(hi4(q))}}; }
+__device__ __forceinline__ f32x4 mfma_block_whole(const Halves& a, const Halves& b) {
+    f32x4 c[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const u32x8 x = e4m3_halves(u ? hi4(a) : lo4(a)), y = e4m3_halves(u ? hi4(b) : lo4(b));
-        c = mfma_dense<F16T>(lo4(x), lo4(y), c);
-        c = mfma_dense<F16T>(hi4(x), hi4(y), c);
+    for (int u = 0; u < 4; ++u) {
+        const u32x8 x = a.v[u / 2], y = b.v[u / 2];
+        c[u] = mfma_dense<F16T>(u & 1 ? hi4(x) : lo4(x), u & 1 ? hi4(y) : lo4(y), u ? c[u - 1] : f32x4{0.f, 0.f, 0.f, 0.f});
+        // (alive till here: its registers and the result's are the same or apart, never some of them shared, which waits)
+        if (u) asm volatile("" ::"v"(c[u - 1]));
     }
-    return c;
+    return c[3];
 }
 
 // ---- rows to E4M3 ----

@@ -52,6 +52,12 @@ struct ScaledArgs {
     int32_t nsplit;
 };
 
+// Whether no product of the sums may lose bits.  The 8-bit matrix instruction is off by 1.5e-5 of a result's norm, a
+// hundredth of a bfloat16 rounding and a fourteenth of a binary16 one.  A value that becomes E4M3 lands on the other
+// neighbour, an eighth of itself away, where it lies that near a tie: one in a few thousand does, and a feed-forward part in
+// binary16 is then 1e-3 of its norm from its definition, five times its rounding.
+inline bool whole_sums(int32_t y_dtype) { return y_dtype == HTS_FP8_E4M3; }
+
 // The kernels of a product.  Streaming: 16 outputs a workgroup, up to kScaledStreamRows rows.  RING_*, TILE_*: rows of W
 // (gated: half of them gate, half up) x rows of X a workgroup.
 constexpr int64_t kScaledStreamRows = 32;
@@ -61,8 +67,9 @@ enum ScaledKernel {
     TILE_128x128, TILE_256x128, TILE_256x256,
     SCALED_KERNELS
 };
-// Those whose workgroups hold whole blocks of 128 outputs make E4M3 rows themselves; the others leave their sums in a.part.
-inline bool writes_e4m3(ScaledKernel k) { return k == TILE_256x128 || k == TILE_256x256; }
+// One whose workgroups hold whole blocks of 128 outputs makes E4M3 rows itself; the others leave their sums in a.part.
+// (TILE_256x256 has no whole sums: its accumulators and converted operands are more than a wave's registers.)
+inline bool writes_e4m3(ScaledKernel k) { return k == TILE_256x128; }
 hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s);
 // The same on rows that its workgroups make themselves (a.X in x_dtype, a.xs unused): gated of HTS_F16 or HTS_BF16 rows, plain
 // of HTS_F32 rows.  Few rows, and few blocks of them: they lie in LDS.

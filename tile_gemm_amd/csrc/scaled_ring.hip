@@ -11,8 +11,8 @@
 // us for 48 KB of copies, LDS reads and products that only partly overlap: 200 x 5000 x 5136, 26 MB, 20.4 us, the matrix cores
 // busy 10%.  Rows that are no whole number of cache lines apart cost about a sixth (gated 333 x 5504: K = 4096 36.6 us, 4144 43.0).
 // Measured against this form (us): two kernels back to back in place of the ring, 24 x 32001 x 4096 54.9 and 48 rows of two
-// 13824 x 5120 82; operands read a step ahead, no difference; products whole in 16 bits (mfma_block_whole), 64 x 11008 x 4096
-// gated 27.1 to 31.2.
+// 13824 x 5120 82; operands read a step ahead, no difference.  Whole sums (WHOLE: E4M3 rows) make a step longer, 0.92 to 1.22
+// us for 128 x 64: 64 x 11008 x 4096 gated 24.2 (16-bit rows) and 31.2, 48 x 13824 x 5120 32.8 and 40.5.
 #include "scaled_device.h"
 
 namespace hts {
@@ -60,7 +60,7 @@ struct RingShape {
     static_assert(NST >= 2 && (NST - 1) * C < 64 && TOTAL <= 160 * 1024 && NW <= 16, "ring");
 };
 
-template <bool GATED, bool ONCE, int AB, int NB, int WN, int WM, int WK, int NST>
+template <bool GATED, bool ONCE, bool WHOLE, int AB, int NB, int WN, int WM, int WK, int NST>
 __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const ScaledArgs a, int NBK, int MBK) {
     using T = RingShape<AB, NB, WN, WM, WK, NST>;
     static_assert(!GATED || AB % 2 == 0, "gate and up");
@@ -168,15 +168,22 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
         copy(t + NST - 1, free);
         const float w0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[0]), t & 63));
         const float w1 = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv[1]), t & 63)) : w0;
+        Halves AH[AB];
+        if (WHOLE)
 #pragma unroll
-        for (int c = 0; c < NB; ++c)
+            for (int b = 0; b < AB; ++b) AH[b] = e4m3_halves(A[b]);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            Halves BH;
+            if (WHOLE) BH = e4m3_halves(B[c]);
 #pragma unroll
             for (int b = 0; b < AB; ++b) {
-                const f32x4 p = mfma_block(A[b], B[c]);
+                const f32x4 p = WHOLE ? mfma_block_whole(AH[b], BH) : mfma_block(A[b], B[c]);
                 const float s = sx[c] * (GATED && b >= HB ? w1 : w0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[b][c][e] = __builtin_fmaf(p[e], s, acc[b][c][e]);
             }
+        }
         free = st;
         st = st + T::STAGE == NST * T::STAGE ? 0 : st + T::STAGE;
     }
@@ -229,10 +236,10 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void scaled_ring_kernel(const Sc
     }
 }
 
-template <bool GATED, bool ONCE, int AB, int NB, int WN, int WM, int WK, int NST>
+template <bool GATED, bool ONCE, bool WHOLE, int AB, int NB, int WN, int WM, int WK, int NST>
 hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
     using T = RingShape<AB, NB, WN, WM, WK, NST>;
-    auto kern = scaled_ring_kernel<GATED, ONCE, AB, NB, WN, WM, WK, NST>;
+    auto kern = scaled_ring_kernel<GATED, ONCE, WHOLE, AB, NB, WN, WM, WK, NST>;
     static DeviceOnce lds_limit;
     hipError_t e = lds_limit.run([&] {
         return hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, T::TOTAL);
@@ -247,12 +254,17 @@ hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
 // Weights of 64 MB and more, rows of whole cache lines, and one row of workgroups for all rows of X: each line is read once, and
 // no other call finds it in the caches (24 x 32001 x 4096: 27.6 us, 31.0 without; 48 rows of two 13824 x 5120: 32.8 and 36.1.
 // On rows of 5136, whose lines two steps share, 45.2 and 43.4; 16 x 11008 x 4096 called again and again 12.8 and 11.5).
+template <bool GATED, bool WHOLE, int AB, int NB, int WN, int WM, int WK, int NST>
+hipError_t launch_sums(const ScaledArgs& a, hipStream_t s) {
+    bool once = a.M <= 16 * NB * WM && a.N * a.K * (GATED ? 2 : 1) >= int64_t(64) << 20;
+    for (int w = 0; w < (GATED ? 2 : 1); ++w) once = once && a.ldw[w] % 128 == 0 && reinterpret_cast<uintptr_t>(a.W[w]) % 128 == 0;
+    return once ? launch_shape<GATED, true, WHOLE, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<GATED, false, WHOLE, AB, NB, WN, WM, WK, NST>(a, s);
+}
 template <int AB, int NB, int WN, int WM, int WK, int NST>
 hipError_t launch_any(const ScaledArgs& a, hipStream_t s) {
-    bool once = a.M <= 16 * NB * WM && a.N * a.K * (a.gated ? 2 : 1) >= int64_t(64) << 20;
-    for (int w = 0; w < (a.gated ? 2 : 1); ++w) once = once && a.ldw[w] % 128 == 0 && reinterpret_cast<uintptr_t>(a.W[w]) % 128 == 0;
-    if (a.gated) return once ? launch_shape<true, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<true, false, AB, NB, WN, WM, WK, NST>(a, s);
-    return once ? launch_shape<false, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<false, false, AB, NB, WN, WM, WK, NST>(a, s);
+    const bool whole = whole_sums(a.y_dtype);
+    if (a.gated) return whole ? launch_sums<true, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_sums<true, false, AB, NB, WN, WM, WK, NST>(a, s);
+    return whole ? launch_sums<false, true, AB, NB, WN, WM, WK, NST>(a, s) : launch_sums<false, false, AB, NB, WN, WM, WK, NST>(a, s);
 }
 
 }  // namespace

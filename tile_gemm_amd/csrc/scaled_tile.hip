@@ -14,6 +14,13 @@
 // the instructions 568; operands two column blocks ahead 561; outputs through LDS in whole lines 543 to 491, 3000 x 20000 x
 // 1024 114 to 85 (32 bytes of a line at a time wrote 368 MB for 226).  Measured and dropped: W from memory straight into
 // registers (256 x 192: 918 for 568), lines touched ahead, the order of K turned per workgroup (563 to 607 for 571).
+//
+// WHOLE (E4M3 rows): the operands become binary16 values in registers and a piece takes four 16-bit instructions, 64 cycles for
+// 32.  Such an instruction leaves the vector units no room (measured: one and n vector operations behind it take 17 + 4 n
+// cycles), so that a block of 256 x 128 takes its 2048 cycles of matrix instructions and, behind one another, the 1900
+// of conversions and additions: 1.6 to 1.9 us.  2048 x 11008 x 4096 gated 359 us, 1.03 PFLOP/s (a 16-bit library
+// product of 8192 cubed: 1.21).  Measured and dropped: a block in two halves of 64 columns with the conversions spread
+// evenly over its pieces, whose sums are scaled twice, 389.
 #include "scaled_device.h"
 
 namespace hts {
@@ -100,7 +107,7 @@ __device__ __forceinline__ void block_of(int id, int NB, int MB, int& nb, int& m
     mb = in / n;
 }
 
-template <bool GATED, int WN, int WM, int BM>
+template <bool GATED, bool WHOLE, int WN, int WM, int BM>
 __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const ScaledArgs a, int NB, int MB) {
     using T = TileShape<WN, WM, BM>;
     constexpr int NW = T::NW, NBJ = T::NBJ, BNO = GATED ? T::BN / 2 : T::BN, RW = GATED ? 32 : 64;
@@ -186,7 +193,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     const uint32_t abase = wn * 8192 + i * 128, bbase = T::XOFF + wm * T::WTM * 128 + i * 128;
     const uint32_t sbase = T::SOFF + 4 * (wm * T::WTM + NBJ * i);
 
-    // One block's sums: step t = 4 bj + b makes the piece (b, bj) and adds the scaled piece of step t - 3, whose matrix
+    // One block's sums: step t = 4 bj + b makes the piece (b, bj) (WHOLE: W is converted during the first column, the next
+    // column of X during each) and adds the scaled piece of step t - 3, whose matrix
     // instruction has ended by then.  B of column block bj + 2 is read during bj (one ahead, the reads came too late:
     // LDS answers after more than four matrix instructions), the next block's first two and its A during the last two.  Two
     // barriers a block say what has landed and what has been read by all: one before the first read of the columns from H
@@ -196,6 +204,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     auto read_b = [&](uint32_t st, int bj) { return cat8(ld16(smem + st + bbase + 2048 * bj + c0), ld16(smem + st + bbase + 2048 * bj + c1)); };
     auto read_s = [&](uint32_t st, int bj) { return *reinterpret_cast<const float*>(smem + st + sbase + 4 * bj); };
     u32x8 A[4], B[2];
+    Halves AH[4], BH, BN;
     float sx[2];
     f32x4 p[4];
     float s0 = 0.f, s1 = 0.f;          // scales of the pieces not yet added
@@ -219,6 +228,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
             B[bj] = read_b(st, bj);
             sx[bj] = read_s(st, bj);
         }
+        if (WHOLE) BH = e4m3_halves(B[0]);
     }
     for (int kb = kb0; kb < kb1; ++kb) {
         if (((kb - kb0) & 63) == 0) load_ws(kb);
@@ -238,7 +248,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int last = bj == 0 ? NBJ - 1 : bj - 1;
-                p[b] = mfma_block(A[b], B[0]);
+                if constexpr (WHOLE) {
+                    if (bj == 0) AH[b] = e4m3_halves(A[b]);
+                    p[b] = mfma_block_whole(AH[b], BH);
+                    if (b & 1) BN.v[b / 2] = e4m3_halves(b / 2 ? hi4(B[1]) : lo4(B[1]));
+                } else {
+                    p[b] = mfma_block(A[b], B[0]);
+                }
                 if (bj + 1 == NBJ) A[b] = read_a(sn, b);
                 // the copies of block kb + 2 go between the matrix instructions, into what has been read
                 constexpr int FIRST = T::H - 2, SLOTS = 4 * (NBJ - T::H);
@@ -255,6 +271,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
             s1 = t1;
             B[0] = B[1];
             B[1] = Bn;
+            if (WHOLE) BH = BN;
             sx[0] = sx[1];
             sx[1] = sn2;
         }
@@ -288,7 +305,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
                     const float h = act_value(a.act, acc[b][bj][e]) * acc[b + 2][bj][e];
                     acc[b][bj][e] = nr + 16 * b + 4 * g + e < a.N ? h : 0.f;
                 }
-        if constexpr (BNO == 128) {
+        if constexpr (WHOLE && BNO == 128) {
             if (a.y_dtype == HTS_FP8_E4M3) {
                 static_assert(BM * BNO + WN * BM * 4 <= T::TOTAL, "the rows and their largest values fit");
                 float* tops = reinterpret_cast<float*>(smem + BM * BNO);
@@ -349,10 +366,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void scaled_tile_kernel(const Scal
     }
 }
 
-template <bool GATED, int WN, int WM, int BM>
+template <bool GATED, bool WHOLE, int WN, int WM, int BM>
 hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
     using T = TileShape<WN, WM, BM>;
-    auto kern = scaled_tile_kernel<GATED, WN, WM, BM>;
+    auto kern = scaled_tile_kernel<GATED, WHOLE, WN, WM, BM>;
     static DeviceOnce lds_limit;
     hipError_t e = lds_limit.run([&] {
         return hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, T::TOTAL);
@@ -364,13 +381,19 @@ hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool WHOLE, int WN, int WM, int BM>
+hipError_t launch_sums(const ScaledArgs& a, hipStream_t s) {
+    return a.gated ? launch_shape<true, WHOLE, WN, WM, BM>(a, s) : launch_shape<false, WHOLE, WN, WM, BM>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_scaled_tile(const ScaledArgs& a, ScaledKernel k, hipStream_t s) {
     if (a.y_dtype == HTS_FP8_E4M3 && !a.part && !writes_e4m3(k)) return hipErrorInvalidValue;
-    if (k == TILE_256x256) return a.gated ? launch_shape<true, 4, 2, 256>(a, s) : launch_shape<false, 4, 2, 256>(a, s);
-    if (k == TILE_256x128) return a.gated ? launch_shape<true, 4, 2, 128>(a, s) : launch_shape<false, 4, 2, 128>(a, s);
-    if (k == TILE_128x128) return a.gated ? launch_shape<true, 2, 2, 128>(a, s) : launch_shape<false, 2, 2, 128>(a, s);
+    const bool whole = whole_sums(a.y_dtype);
+    if (k == TILE_256x256) return whole ? hipErrorInvalidValue : launch_sums<false, 4, 2, 256>(a, s);
+    if (k == TILE_256x128) return whole ? launch_sums<true, 4, 2, 128>(a, s) : launch_sums<false, 4, 2, 128>(a, s);
+    if (k == TILE_128x128) return whole ? launch_sums<true, 2, 2, 128>(a, s) : launch_sums<false, 2, 2, 128>(a, s);
     return hipErrorInvalidValue;
 }
 
