@@ -498,14 +498,15 @@ hts_status hts_quantize_weight(int32_t dtype, int64_t N, int64_t K, const void* 
 
 /* Device, asynchronous.  The block-scaled product
  *     Y[m,n] = sum_b x_scale[b,m] * w_scale[n/128,b] * sum_{k in b} X[m,k] * W[n,k]
- * Y as HTS_F32, HTS_F16 or HTS_BF16, ldy >= N a multiple of 4, 16-byte aligned, any N.  Each block's sum is made by
- * one 8-bit matrix instruction, which keeps, in every group of eight products, 13 bits below the largest one's
- * power of two; the scaled sums are added in 32 bits and rounded once.  For values spread as a quantised normal
- * distribution that is an error of 1.5e-5 in the 2-norm, also of an HTS_F32 output.  The product of the two scales
- * is 32-bit too.  A NaN value, or a NaN or infinite scale, makes its row or column of Y NaN or infinite.
+ * Y as HTS_F32, HTS_F16 or HTS_BF16, ldy >= N a multiple of 4, 16-byte aligned, any N, all sums in 32 bits and
+ * rounded once.  For a 16-bit Y each block's sum is made by one 8-bit matrix instruction, which keeps, in every group of
+ * eight products, 13 bits below the largest one's power of two: for values spread as a quantised normal distribution
+ * an error of 1.5e-5 in the 2-norm, a fourteenth of HTS_F16's rounding.  For HTS_F32 no product loses bits (16-bit
+ * matrix instructions: twice the time where those set the pace) and the error is that of 32-bit sums, 2e-7.  The
+ * product of the two scales is 32-bit too.  A NaN value, or a NaN or infinite scale, makes its row or column of Y NaN or infinite.
  * Rows past M are not read, and Y must not overlap what is read.  M == 0 is a no-op.  workspace:
- * hts_scaled_gemm_workspace() bytes, 16-byte aligned, or NULL: with less the product runs unsplit, with another order of its 32-bit sums.  Results are deterministic for a given
- * shape and workspace.  Calls that share a workspace must not overlap. */
+ * hts_scaled_gemm_workspace() bytes (for any y_dtype), 16-byte aligned, or NULL: with less the product runs unsplit, with
+ * another order of its 32-bit sums.  Results are deterministic for a given shape and workspace.  Calls that share a workspace must not overlap. */
 hts_status hts_scaled_gemm(int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const float* x_scale,
                            int64_t ldxs, const hts_scaled_weight* W, void* Y, int64_t ldy, int32_t y_dtype,
                            void* workspace, size_t workspace_bytes, void* stream);
@@ -519,10 +520,10 @@ enum { HTS_ACT_SILU = 0, HTS_ACT_GELU = 1, HTS_ACT_GELU_TANH = 2 };
  *   h_dtype HTS_F32, HTS_F16, HTS_BF16 : h_scale must be NULL; ldh >= N a multiple of 4, any N
  *   h_dtype HTS_FP8_E4M3               : H rows of values and h_scale [ceil(N/128), ldhs] as hts_quantize_rows makes
  *                                        them of the unrounded H; N and ldh multiples of 16.  The next product's X.
- *                                        The sums behind them lose no products: a value is its definition's E4M3
- *                                        neighbour unless it lies nearer to a tie than a 32-bit sum is exact.
+ *                                        A value is its definition's E4M3 neighbour unless it lies nearer to a tie
+ *                                        than 32-bit sums are exact.
  * workspace: hts_scaled_gated_workspace() bytes; optional, but for HTS_FP8_E4M3, which may need all of them
- * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm. */
+ * (HTS_ERR_WORKSPACE).  Otherwise as hts_scaled_gemm; for HTS_FP8_E4M3 as for HTS_F32 no product loses bits. */
 hts_status hts_scaled_gated(int32_t act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
                             const float* x_scale, int64_t ldxs, const hts_scaled_weight* gate,
                             const hts_scaled_weight* up, void* H, int64_t ldh, int32_t h_dtype, float* h_scale,

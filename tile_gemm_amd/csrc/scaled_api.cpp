@@ -151,7 +151,8 @@ float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weight
     return us;
 }
 
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int32_t y_dtype) {
+// most: bytes that the parts may take.
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int32_t y_dtype, uint64_t most = ~uint64_t(0)) {
     const bool out8 = y_dtype == HTS_FP8_E4M3, whole = hts::whole_sums(y_dtype);
     Plan p{};
     p.ldp = (N + 3) / 4 * 4;
@@ -165,13 +166,15 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated, int32_t y_dtype) {
         for (int split = 1; split <= 8; split *= 2) {
             if (split > KB || (split > 1 && k == hts::SCALED_STREAM)) break;
             const bool parts = split > 1 || (out8 && !hts::writes_e4m3(k));
+            const uint64_t bytes = parts ? (uint64_t)split * weights * M * p.ldp * 4 : 0;
+            if (bytes > most) break;
             const float us = estimate(k, M, N, KB, weights, split, whole) + (parts ? 3.0f + split * plane : 0.0f);
             if (!p.nsplit || us < best) {
                 best = us;
                 p.kernel = k;
                 p.nsplit = split;
                 p.need = out8 && !hts::writes_e4m3(k);
-                p.bytes = parts ? (uint64_t)split * weights * M * p.ldp * 4 : 0;
+                p.bytes = bytes;
             }
         }
     }
@@ -294,7 +297,9 @@ hts_status hts_scaled_gemm(int64_t M, int64_t N, int64_t K, const void* X, int64
     a.Y = Y;
     a.ldy = ldy;
     a.y_dtype = y_dtype;
-    return run(a, plan_of(M, N, K, false, y_dtype), workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+    // one workspace for outputs of any type: what a 16-bit one takes
+    const uint64_t most = y_dtype == HTS_F32 ? plan_of(M, N, K, false, HTS_BF16).bytes : ~uint64_t(0);
+    return run(a, plan_of(M, N, K, false, y_dtype, most), workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 hts_status hts_scaled_gemm_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes) {

@@ -53,10 +53,11 @@ struct ScaledArgs {
 };
 
 // Whether no product of the sums may lose bits.  The 8-bit matrix instruction is off by 1.5e-5 of a result's norm, a
-// hundredth of a bfloat16 rounding and a fourteenth of a binary16 one.  A value that becomes E4M3 lands on the other
+// hundredth of a bfloat16 rounding and a fourteenth of a binary16 one, and a hundred times what 32-bit sums are off by: an
+// HTS_F32 output would show all of it.  A value that becomes E4M3 lands on the other
 // neighbour, an eighth of itself away, where it lies that near a tie: one in a few thousand does, and a feed-forward part in
 // binary16 is then 1e-3 of its norm from its definition, five times its rounding.
-inline bool whole_sums(int32_t y_dtype) { return y_dtype == HTS_FP8_E4M3; }
+inline bool whole_sums(int32_t y_dtype) { return y_dtype == HTS_F32 || y_dtype == HTS_FP8_E4M3; }
 
 // The kernels of a product.  Streaming: 16 outputs a workgroup, up to kScaledStreamRows rows.  RING_*, TILE_*: rows of W
 // (gated: half of them gate, half up) x rows of X a workgroup.

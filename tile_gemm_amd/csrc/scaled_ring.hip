@@ -11,7 +11,7 @@
 // us for 48 KB of copies, LDS reads and products that only partly overlap: 200 x 5000 x 5136, 26 MB, 20.4 us, the matrix cores
 // busy 10%.  Rows that are no whole number of cache lines apart cost about a sixth (gated 333 x 5504: K = 4096 36.6 us, 4144 43.0).
 // Measured against this form (us): two kernels back to back in place of the ring, 24 x 32001 x 4096 54.9 and 48 rows of two
-// 13824 x 5120 82; operands read a step ahead, no difference.  Whole sums (WHOLE: E4M3 rows) make a step longer, 0.92 to 1.22
+// 13824 x 5120 82; operands read a step ahead, no difference.  Whole sums (WHOLE: E4M3 and 32-bit rows) make a step longer, 0.92 to 1.22
 // us for 128 x 64: 64 x 11008 x 4096 gated 24.2 (16-bit rows) and 31.2, 48 x 13824 x 5120 32.8 and 40.5.
 #include "scaled_device.h"
 

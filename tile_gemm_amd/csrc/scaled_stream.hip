@@ -229,8 +229,11 @@ hipError_t launch_mg(const ScaledArgs& a, hipStream_t s) {
 hipError_t launch_scaled_stream(const ScaledArgs& a, hipStream_t s) {
     if (a.M > kScaledStreamRows || (a.y_dtype == HTS_FP8_E4M3 && !a.part)) return hipErrorInvalidValue;
     constexpr int E4M3 = HTS_FP8_E4M3;
-    // whole sums of two weights: one block ahead at any K (13824 x 5120, one row: 41.2 us with four, 34.2)
-    if (a.gated && a.part) return a.M <= 16 ? launch_rows<true, 1, 1, E4M3, true>(a, s) : launch_rows<true, 1, 2, E4M3, true>(a, s);
+    if (whole_sums(a.y_dtype)) {
+        // two weights: one block ahead at any K (E4M3 rows, 1 x 13824 x 5120: 34.2 us, 41.2 with four)
+        if (a.gated) return a.M <= 16 ? launch_rows<true, 1, 1, E4M3, true>(a, s) : launch_rows<true, 1, 2, E4M3, true>(a, s);
+        return a.M <= 16 ? launch_mg<false, 1, E4M3, true>(a, s) : launch_mg<false, 2, E4M3, true>(a, s);
+    }
     if (a.gated) return a.M <= 16 ? launch_mg<true, 1>(a, s) : launch_mg<true, 2>(a, s);
     return a.M <= 16 ? launch_mg<false, 1>(a, s) : launch_mg<false, 2>(a, s);
 }

@@ -15,7 +15,7 @@
 // 1024 114 to 85 (32 bytes of a line at a time wrote 368 MB for 226).  Measured and dropped: W from memory straight into
 // registers (256 x 192: 918 for 568), lines touched ahead, the order of K turned per workgroup (563 to 607 for 571).
 //
-// WHOLE (E4M3 rows): the operands become binary16 values in registers and a piece takes four 16-bit instructions, 64 cycles for
+// WHOLE (E4M3 and 32-bit rows): the operands become binary16 values in registers and a piece takes four 16-bit instructions, 64 cycles for
 // 32.  Such an instruction leaves the vector units no room (measured: one and n vector operations behind it take 17 + 4 n
 // cycles), so that a block of 256 x 128 takes its 2048 cycles of matrix instructions and, behind one another, the 1900
 // of conversions and additions: 1.6 to 1.9 us.  2048 x 11008 x 4096 gated 359 us, 1.03 PFLOP/s (a 16-bit library

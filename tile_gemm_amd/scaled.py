@@ -169,8 +169,9 @@ def scaled_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: ScaledWeight, out_dty
                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
     """y [M, N] = (x * x_scale) (w)^T from 8-bit values, block by block of K, summed in 32 bits and rounded once to
-    bfloat16, float16 or float32 (whose error is that of the 8-bit matrix instruction, 1.5e-5).  The workspace of a
-    split product is allocated here when none is given."""
+    bfloat16, float16 or float32.  16-bit outputs come from 8-bit matrix instructions (1.5e-5 of the 2-norm, below their
+    rounding); float32 ones lose no products, at up to twice the time.  The workspace of a split product is allocated
+    here when none is given."""
     M, ldx, lds = _rows(x, x_scale, w)
     dev, N = w.gpu, w.N
     out, ldy, dt = _out(out, out_dtype, M, N, _OUT, dev, w.device)
