@@ -60,8 +60,10 @@ class ScaledWeight:
         if self.N == 1 and self.K > 1 and values.stride(1) != 1:
             _bad("values must be contiguous along their rows", 3)
         lds = _lead(scale, "scale", _blocks(self.N), _blocks(self.K), torch.float32, dev)
+        if lds < _blocks(self.K):
+            _bad(f"scale's rows are {lds} apart and {_blocks(self.K)} long (an expanded scale: scale.contiguous())", 3)
         self.values, self.scale, self.device, self.gpu = values, scale, values.device, dev
-        self.desc = _c.hts_scaled_weight(values.data_ptr(), ld, scale.data_ptr(), max(lds, _blocks(self.K)))
+        self.desc = _c.hts_scaled_weight(values.data_ptr(), ld, scale.data_ptr(), lds)
         self._desc = ctypes.byref(self.desc)
         self._workspace = {}     # bytes by (rows, what)
         # the shape's checks, once, before any product uses it
