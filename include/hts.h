@@ -472,7 +472,7 @@ hts_status hts_residual_norm(const hts_norm_desc* d, int64_t M, int64_t N, const
  *   weights : values E4M3 [N, K], leading dimension a multiple of 16; scale float [ceil(N / 128), lds], lds >= KB:
  *             the scale of rows 128 r .. 128 r + 127 and block b at r*lds + b
  * Values are 16-byte aligned, scales 4-byte.  K is a multiple of 16 (a 16-byte chunk of a row), and leading
- * dimensions of values are below 2^22.  M and N are below 2^26, and M * N below 2^36.
+ * dimensions of values are below 2^22.  M and N are below 2^26, and ceil(M / 128) * ceil(N / 128) is below 2^22.
  * ------------------------------------------------------------------------------------------ */
 
 /* A weight (a host structure; values and scale are device memory). */

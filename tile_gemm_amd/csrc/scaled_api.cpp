@@ -26,7 +26,7 @@ hts_status check_shape(int64_t M, int64_t N, int64_t K) {
     if (K >= kMaxLead) return fail(HTS_ERR_UNSUPPORTED, "K=%lld is not below 2^22", (long long)K);
     // a launch takes fewer than 2^32 threads in an axis
     if (N >= kMaxRows || M >= kMaxRows || ((N + 127) / 128) * ((M + 127) / 128) >= kMaxTiles)
-        return fail(HTS_ERR_UNSUPPORTED, "M=%lld N=%lld: too many tiles", (long long)M, (long long)N);
+        return fail(HTS_ERR_UNSUPPORTED, "M=%lld N=%lld: below 2^26 each, ceil(M / 128) * ceil(N / 128) below 2^22", (long long)M, (long long)N);
     return HTS_OK;
 }
 
