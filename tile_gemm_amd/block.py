@@ -10,8 +10,9 @@ back to back:
 
 with every W either a packed hybrid weight (hts_gemm), a row-major dense one
 (hts_dense_gemm, the same-library baseline) or a dense 8-bit one with a scale for each block of 128
-(ScaledWeight: its input is quantised by hts_quantize_rows and multiplied by hts_scaled_gemm).  In ``forward`` the output projection reads A = q in
-place of the attention output, which keeps the shapes and the data dependence of the block.
+(ScaledWeight: the projections of one input share its hts_quantize_rows and go through hts_scaled_gemm; 8-bit
+gate and up through hts_scaled_gated, and with an 8-bit down through hts_scaled_mlp).  In ``forward`` the output projection
+reads A = q in place of the attention output, which keeps the shapes and the data dependence of the block.
 Every call is enqueued on the current stream, so the whole step can be captured in one HIP
 graph.
 
@@ -89,11 +90,14 @@ def forward(X: torch.Tensor, weights: Dict[str, object], bufs: Dict[str, torch.T
             fused: bool = False) -> torch.Tensor:
     """One block step on M = X.shape[0] tokens; returns the down-projection output.  fused (packed
     up weight only): the up product writes silu(gate) * up itself (hts_gemm_silu_mul) instead of
-    writing up for a separate elementwise pass."""
+    writing up for a separate elementwise pass.  8-bit gate and up weights take the steps that ``decode`` takes
+    (the buffers of steps inside a call are then not written)."""
     fuse = fused and isinstance(weights["up"], PackedWeight)
-    for name in ("q", "k", "v", "gate") + (() if fuse else ("up",)):
-        _linear(X, weights[name], bufs[name])
+    scaled = isinstance(weights["gate"], ScaledWeight) and isinstance(weights["up"], ScaledWeight)
+    _linears(X, ("q", "k", "v") + (() if scaled else ("gate",)) + (() if scaled or fuse else ("up",)), weights, bufs)
     _linear(bufs["q"], weights["o"], bufs["o"])          # attention output stand-in: A = q
+    if scaled:
+        return _mlp(X, weights, bufs)
     if fuse:
         gemm_silu_mul(X, weights["up"], bufs["gate"], out=bufs["h"])
     else:
