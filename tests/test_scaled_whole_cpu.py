@@ -4,7 +4,7 @@ import subprocess
 import pytest
 
 from scaled_cases import SHAPES
-from scaled_whole_cases import E4M3_ROWS
+from scaled_whole_cases import E4M3_ROWS, ONCE
 from test_host_sanitize_scaled import HERE, ROOT, _hipcc, _run, driver  # noqa: F401
 
 NAMES = ["stream", "ring 32x16", "ring 64x16", "ring 32x32", "ring 64x32", "ring 64x64", "ring 128x64", "ring 128x128",
@@ -50,3 +50,16 @@ def test_the_gpu_tests_reach_every_kernel_of_32_bit_outputs(f32_driver):
         reached = {NAMES[k] for k, _ in got}
         assert reached == set(NAMES), (gated, sorted(set(NAMES) - reached), list(zip(SHAPES, got)))
         assert any(s > 1 for _, s in got) and any(s == 1 for _, s in got)
+
+
+def test_the_gpu_tests_reach_every_ring_on_weights_read_once(driver, f32_driver):  # noqa: F811
+    rows = {"ring 32x16": 16, "ring 64x16": 16, "ring 32x32": 32, "ring 64x32": 32, "ring 64x64": 64, "ring 128x64": 64, "ring 128x128": 128}
+    for (op, out), shapes in ONCE.items():
+        gated = int(op == "gated")
+        if out == "32":
+            got = _kernels(f32_driver, [v for s in shapes for v in (*s, gated)])
+        else:
+            got = _kernels(driver, [v for s in shapes for v in (*s, gated, int(out == "8"))])
+        names = [NAMES[k] for k, _ in got]
+        assert set(names) == set(rows) - ({"ring 128x128"} if out != "16" else set()), (op, out, names)
+        assert all(M <= rows[n] and N * K * (1 + gated) >= 64 << 20 for n, (M, N, K) in zip(names, shapes))

@@ -256,6 +256,8 @@ hipError_t launch_shape(const ScaledArgs& a, hipStream_t s) {
 // On rows of 5136, whose lines two steps share, 45.2 and 43.4; 16 x 11008 x 4096 called again and again 12.8 and 11.5).
 template <bool GATED, bool WHOLE, int AB, int NB, int WN, int WM, int WK, int NST>
 hipError_t launch_sums(const ScaledArgs& a, hipStream_t s) {
+    // (with whole sums, weights of that size and up to 128 rows run on smaller rings or on tiles)
+    if constexpr (WHOLE && NB * WM == 8) return launch_shape<GATED, false, WHOLE, AB, NB, WN, WM, WK, NST>(a, s);
     bool once = a.M <= 16 * NB * WM && a.N * a.K * (GATED ? 2 : 1) >= int64_t(64) << 20;
     for (int w = 0; w < (GATED ? 2 : 1); ++w) once = once && a.ldw[w] % 128 == 0 && reinterpret_cast<uintptr_t>(a.W[w]) % 128 == 0;
     return once ? launch_shape<GATED, true, WHOLE, AB, NB, WN, WM, WK, NST>(a, s) : launch_shape<GATED, false, WHOLE, AB, NB, WN, WM, WK, NST>(a, s);
