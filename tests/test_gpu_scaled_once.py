@@ -1,5 +1,6 @@
 """Products whose weights of 64 MiB and more are read once: every ring kernel, on rows of whole cache lines (read past
-the caches) and on rows that are not; and what the 8-bit instruction's dropped bits come to in 16-bit outputs."""
+the caches) and on rows that are not; what the 8-bit instruction's dropped bits come to in 16-bit outputs; and rows that
+do not depend on the others of their batch."""
 import pytest
 import torch
 
@@ -8,7 +9,7 @@ import tile_gemm_amd as hts
 import scaled_ref as ref
 import scaled_whole as whole
 from scaled_ref import DEV, E4M3
-from scaled_whole_cases import ONCE
+from scaled_whole_cases import ONCE, PARTS_OF_BATCHES
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,18 @@ def test_16_bit_outputs_are_off_by_little_more_than_their_rounding(M, N, K):
     moved = float((0.8 * 2.1e-5 * size / step).clamp_max(1.0).sum())
     got = int((y.double() != want.to(F16).double()).sum())
     assert got <= 1.05 * moved + 6 * moved ** 0.5, (got, moved)
+
+
+@pytest.mark.parametrize("rows,part,N,K", PARTS_OF_BATCHES)
+def test_a_row_does_not_depend_on_the_others(rows, part, N, K):
+    """In a batch, in a part of it and among rows of NaN: the same bits (one kernel)."""
+    g = ref.generator(rows)
+    x, xs = ref.random_rows(g, rows, K)
+    w = hts.ScaledWeight(*ref.random_weight(g, N, K))
+    y = hts.scaled_gemm(x, xs, w, out_dtype=BF16)
+    first = rows - part
+    again = hts.scaled_gemm(x[first:], xs[first:].t().contiguous().t(), w, out_dtype=BF16)
+    assert torch.equal(again, y[first:])
+    x = x.clone()
+    x.view(torch.uint8)[:first] = 0x7F
+    assert torch.equal(hts.scaled_gemm(x, xs, w, out_dtype=BF16)[first:], y[first:])

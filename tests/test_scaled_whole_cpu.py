@@ -4,7 +4,7 @@ import subprocess
 import pytest
 
 from scaled_cases import SHAPES
-from scaled_whole_cases import E4M3_ROWS, ONCE
+from scaled_whole_cases import E4M3_ROWS, ONCE, PARTS_OF_BATCHES
 from test_host_sanitize_scaled import HERE, ROOT, _hipcc, _run, driver  # noqa: F401
 
 NAMES = ["stream", "ring 32x16", "ring 64x16", "ring 32x32", "ring 64x32", "ring 64x64", "ring 128x64", "ring 128x128",
@@ -63,3 +63,9 @@ def test_the_gpu_tests_reach_every_ring_on_weights_read_once(driver, f32_driver)
         names = [NAMES[k] for k, _ in got]
         assert set(names) == set(rows) - ({"ring 128x128"} if out != "16" else set()), (op, out, names)
         assert all(M <= rows[n] and N * K * (1 + gated) >= 64 << 20 for n, (M, N, K) in zip(names, shapes))
+
+
+def test_parts_of_batches_share_their_kernel(driver):  # noqa: F811
+    for rows, part, N, K in PARTS_OF_BATCHES:
+        a, b = _kernels(driver, [rows, N, K, 0, 0, part, N, K, 0, 0])
+        assert a == b, (rows, part, N, K, a, b)
