@@ -56,6 +56,39 @@ __device__ __forceinline__ f32x4 mfma_block_whole(const Halves& a, const Halves&
     return c[3];
 }
 
+// ---- from global memory to registers and LDS ----
+
+typedef __attribute__((address_space(3))) void lds_t;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+// Past every buffer's end (their bytes stay below 2^31): such a lane reads zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// 16 bytes a lane into LDS.  ONCE: what no other workgroup reads claims no place in the caches.
+template <bool ONCE = false>
+__device__ __forceinline__ void copy16(rsrc_t r, uint32_t lds_off, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t*)((lds_u8*)smem + lds_off), 16, voff, soff, 0, ONCE ? 2 : 0);
+}
+__device__ __forceinline__ void copy4(const void* g, uint32_t lds_off) {
+    __builtin_amdgcn_global_load_lds(g, (lds_t*)((lds_u8*)smem + lds_off), 4, 0, 0);
+}
+
+// All but this wave's N youngest copies have landed and its LDS reads are back; then the same of the whole workgroup.
+template <int N>
+__device__ __forceinline__ void landed_but() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));      // lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ---- rows to E4M3 ----
 
 // 16 consecutive values at column c of a row (c and K multiples of 16), as floats.

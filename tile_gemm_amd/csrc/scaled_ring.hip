@@ -18,35 +18,6 @@
 namespace hts {
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_t;
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-
-extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-
-__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-// ONCE: what no other workgroup reads claims no place in the caches.
-template <bool ONCE = false>
-__device__ __forceinline__ void copy16(rsrc_t r, uint32_t lds_off, uint32_t voff, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t*)((lds_u8*)smem + lds_off), 16, voff, soff, 0, ONCE ? 2 : 0);
-}
-__device__ __forceinline__ void copy4(const void* g, uint32_t lds_off) {
-    __builtin_amdgcn_global_load_lds(g, (lds_t*)((lds_u8*)smem + lds_off), 4, 0, 0);
-}
-constexpr uint32_t kOutside = 0x80000000u;   // past every buffer's end (their bytes stay below 2^31): reads zeros
-
-// All but this wave's N youngest copies have landed and its LDS reads are back; then the same of the whole workgroup.
-template <int N>
-__device__ __forceinline__ void landed_but() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));      // lgkmcnt 0
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 // Rows of W and X a workgroup, WK blocks of K a step (one for each group of WN x WM waves), NST steps in the ring.
 template <int AB, int NB, int WN, int WM, int WK, int NST>
 struct RingShape {
