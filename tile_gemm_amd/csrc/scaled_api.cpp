@@ -247,11 +247,12 @@ MlpPlan mlp_plan(int64_t M, int64_t hidden, int64_t inner) {
     p.hs = p.hq + round256((uint64_t)M * inner);
     p.parts = p.hs + round256(4 * (uint64_t)p.lds * scale_blocks(inner));
     p.bytes = p.parts + std::max(p.gated.bytes, p.down.bytes);
-    // Two launches save about 4.7 us of the three or four others, and lose to them with every byte of weights: their
-    // kernel streams slower, and every workgroup makes all rows.  us, two launches against the others: 4096 x 1024, four rows
-    // 11.6 : 15.1; 4096 x 4096, four rows 21.7 : 24.1; 4096 x 11008, one row 35.3 : 35.9, two rows 37.2 : 35.3; 5120 x
-    // 13824, one row 51.9 : 49.6.
-    p.made = 3.0 * hidden * inner * (0.022 + 0.01 * M) < 4.7e6 && M <= hts::kMadeRows &&
+    // Two launches save the others' two or three.  Up to 4096 columns of X the first one keeps one block of loads ahead and
+    // many waves, and they win by 2 to 9 us; beyond, every workgroup's making of the rows and its four blocks
+    // ahead cost with every byte of weights.  us, two launches against the others (hidden x inner, rows): 4096 x 1024, 4
+    // 12.8 : 15.3; 4096 x 11008, 1 34.6 : 42.1, 4 39.0 : 42.2; 4096 x 28672, 1 75.9 : 87.9; 1024 x 28672, 1 34.6 : 32.7; 5120 x
+    // 2816, 4 19.9 : 26.3; 5120 x 8192, 1 35.8 : 36.1, 2 37.8 : 35.8; 5120 x 14336, 1 58.8 : 56.4; 8192 x 5632, 1 39.4 : 36.4.
+    p.made = (hidden <= 4096 || 3.0 * hidden * inner * (0.022 + 0.01 * M) < 4.7e6) && M <= hts::kMadeRows &&
              M * std::max(scale_blocks(hidden), scale_blocks(inner)) <= hts::kMadeBlocks;
     if (p.made) {
         p.parts = 0;
