@@ -91,22 +91,22 @@ struct Plan {
 // The kernel and split with the least estimated time.  A kernel's step (`blocks` of K on rows_n x rows_m) takes `step` us
 // with one workgroup on each of some CUs, and no less than its weights take from memory; workgroups beyond a CU's each (two:
 // TILE_128x128) wait for another round, and a round costs its start and end.  The steps are fitted to every kernel and
-// split timed at 60 sizes; over them the choice takes 1.01 to 1.07 of the best one's time (geometric means).  Both sides of
-// the choices that users meet most (us):
-//   1 x 11008 x 4096 gated          stream 19.1, ring 128x64 20.2      8 rows          stream 20.4, ring 128x64 20.3
-//   32 x 11008 x 4096 gated         ring 128x64 21.7, stream 27.3      16 x 11008 x 4096   ring 64x16 11.3, 64x32 11.8
-//   48 x 13824 x 5120 gated         ring 128x64 33.3, 128x128 36.4     100 rows        ring 128x128 39.9, tile 128x128 45.4
-//   64 x 11008 x 4096               ring 64x64 15.5, 128x64 17.2       32 x 4096 x 11008   ring 32x16 13.0, in two 15.0
-//   128 x 11008 x 4096              ring 128x64 18.0, tile 128x128 in two 22.0
-//   256 x 11008 x 4096              tile 128x128 24.5, ring 128x128 28.9
-//   333 x 5504 x 4144 gated         tile 256x128 43.0, 128x128 45.8    512 x 11008 x 4096  256x256 64.5, 128x128 67.2
-//   2048 x 4096 x 11008             tile 256x128 91.5, 128x128 95, 256x256 120
-//   8192 x 13824 x 5120             tile 256x256 497, 128x128 578, 256x128 586
+// split timed at 49 sizes of 16-bit outputs and 60 of whole sums, the weights from memory; over them the choice takes 1.03
+// and 1.01 of the best one's time (geometric means).  Both sides of the choices that users meet most (us):
+//   1 x 11008 x 4096 gated          ring 128x64 19.4, stream 20.6      8 rows          ring 128x64 19.2, stream 21.9
+//   32 x 11008 x 4096 gated         ring 128x64 20.9, 64x32 25.8       16 x 11008 x 4096   ring 64x16 11.8, 64x32 12.1
+//   48 x 13824 x 5120 gated         ring 128x64 32.6, 128x128 35.7     100 rows        ring 128x128 40.4, tile 128x128 44.7
+//   64 x 11008 x 4096               ring 64x64 17.6, 128x64 in two 20.3    32 x 4096 x 11008   ring 32x16 16.0, 64x32 in four 15.9
+//   128 x 11008 x 4096              ring 128x64 21.4, tile 128x128 in two 23.8
+//   256 x 11008 x 4096              tile 128x128 26.4, ring 128x128 28.4
+//   333 x 5504 x 4144 gated         tile 256x128 54.0, 128x128 45.4 (the farthest off)     512 x 11008 x 4096 gated  256x256 65.1, 128x128 67.9
+//   2048 x 4096 x 11008             tile 256x128 96.0, 128x128 102, 256x256 128
+//   8192 x 13824 x 5120             tile 256x256 519, 128x128 602, 256x128 612
 // Whole sums (`whole` us a step), gated to E4M3 rows, the second launch of those that leave parts included:
-//   1 x 11008 x 4096                stream 24.5, ring 64x16 25.4       4 x 13824 x 5120    ring 64x16 31.0, 64x32 33.6
-//   64 x 11008 x 4096               ring 128x64 31.2, in two 37.4      100 rows        tile 128x128 in two 44.4, in one 44.7
-//   200 x 11008 x 4096              tile 256x128 61.4, 128x128 in two 65.5     512 rows    128x128 109, 256x128 120
-//   2048 x 11008 x 4096             tile 256x128 359, 128x128 371
+//   1 x 11008 x 4096                stream 24.4, ring 64x16 25.4       1 x 13824 x 5120    ring 64x16 30.8, stream 35.5
+//   64 x 11008 x 4096               ring 128x64 31.0, in two 37.7      100 rows        tile 128x128 in two 44.6, ring 128x128 49.7
+//   200 x 11008 x 4096              tile 256x128 61.6, 128x128 in two 66.4     512 rows    128x128 111, 256x128 121
+//   2048 x 11008 x 4096             tile 256x128 363, 128x128 380
 struct Shape {
     int rows_n, rows_m, blocks;
     float step, whole;
@@ -127,7 +127,7 @@ constexpr Shape kShapes[hts::SCALED_KERNELS] = {
 
 float estimate(hts::ScaledKernel k, int64_t M, int64_t N, int64_t KB, int weights, int split, bool whole) {
     if (k == hts::SCALED_STREAM)
-        return 4.0f + std::max(weights * (float)N * KB * 128 / 5.5e6f * (1.0f + M / 40.0f),
+        return 4.0f + std::max(weights * (float)N * KB * 128 / (whole ? 5.1e6f : 5.5e6f) * (1.0f + M / (whole ? 60.0f : 40.0f)),
                                0.35f * (weights + (M + 15) / 16) * ((KB + 7) / 8));     // a wave's loads, one block at a time
     const Shape& s = kShapes[k];
     const int64_t mb = (M + s.rows_m - 1) / s.rows_m;
