@@ -5,8 +5,8 @@
 // instruction, NT blocks of loads ahead of their use; each block's sum is multiplied by both scales and added in 32 bits.
 // The waves' sums meet in LDS and are added in wave order.
 //
-// Bound by the weights' bytes: 1 x 11008 x 4096 with two weights, 90 MB, in 19.1 us, 4.7 TB/s (a streaming read of
-// 131 MB: 5.8 to 6.1); its waves wait for data 68% of their cycles, the vector units are busy 15%.  A small one is latency: 1 x
+// Bound by the weights' bytes: 1 x 11008 x 4096 with two weights, 90 MB, in 20.6 us, 4.4 TB/s (a streaming read of
+// 131 MB: 5.8 to 6.1); its waves wait for data 55% of their cycles, the vector units are busy 15%.  A small one is latency: 1 x
 // 4096 x 4096, 17 MB, 6.7 us, of which the bytes are 3.8.  Measured against this form (us): a wave's blocks in one contiguous
 // run, no difference; loads that claim no place in the caches, none.
 #include "scaled_device.h"

@@ -7,9 +7,9 @@
 // both scales and added to its 32-bit accumulator on the vector units, while the matrix cores make the next ones.
 //
 // 8192 x 13824 x 5120: 497 to 526 us from card to card, 2.2 to 2.3 PFLOP/s; the library's product of the same values without
-// scales takes 434, one of 8192 cubed reaches 2.86 PFLOP/s.  Bound by what a block's 2048 cycles of matrix instructions do not
+// scales takes 419 to 434, one of 8192 cubed reaches 2.86 to 3.09 PFLOP/s.  Bound by what a block's 2048 cycles of matrix instructions do not
 // hide: 3700 to 3900 pass a block (256 x 256), the matrix cores are busy 55%, the vector units, which add the pieces, 48%;
-// returns of LDS reads stand in the way of the matrix instructions, and the clock falls to 1.95 GHz.  Steps that made it
+// returns of LDS reads stand in the way of the matrix instructions, and the clock falls (1.7 GHz of 2.4 while counters are read).  Steps that made it
 // (us): one tile shape, copies a block ahead 642; pieces added three steps behind their instruction, copies between
 // the instructions 568; operands two column blocks ahead 561; outputs through LDS in whole lines 543 to 491, 3000 x 20000 x
 // 1024 114 to 85 (32 bytes of a line at a time wrote 368 MB for 226).  Measured and dropped: W from memory straight into
@@ -18,8 +18,8 @@
 // WHOLE (E4M3 and 32-bit rows): the operands become binary16 values in registers and a piece takes four 16-bit instructions, 64 cycles for
 // 32.  Such an instruction leaves the vector units no room (measured: one and n vector operations behind it take 17 + 4 n
 // cycles), so that a block of 256 x 128 takes its 2048 cycles of matrix instructions and, behind one another, the 1900
-// of conversions and additions: 1.6 to 1.9 us.  2048 x 11008 x 4096 gated 359 us, 1.03 PFLOP/s (a 16-bit library
-// product of 8192 cubed: 1.21).  Measured and dropped: a block in two halves of 64 columns with the conversions spread
+// of conversions and additions: 1.6 to 1.9 us (matrix cores busy 42%, vector units 55%).  2048 x 11008 x 4096 gated 360 us, 1.03
+// PFLOP/s (the library's binary16 product of that size 414, one of 8192 cubed 1.54 PFLOP/s).  Measured and dropped: a block in two halves of 64 columns with the conversions spread
 // evenly over its pieces, whose sums are scaled twice, 389.
 #include "scaled_device.h"
 
