@@ -502,7 +502,7 @@ hts_status hts_quantize_weight(int32_t dtype, int64_t N, int64_t K, const void* 
  * rounded once.  For a 16-bit Y each block's sum is made by one 8-bit matrix instruction, which keeps, in every group of
  * eight products, 13 bits below the largest one's power of two: for values spread as a quantised normal distribution
  * an error of 1.5e-5 in the 2-norm, a fourteenth of HTS_F16's rounding.  For HTS_F32 no product loses bits (16-bit
- * matrix instructions: twice the time where those set the pace) and the error is that of 32-bit sums, 2e-7.  The
+ * matrix instructions: twice the time where those set the pace) and the error is that of 32-bit sums, 1e-7.  The
  * product of the two scales is 32-bit too.  A NaN value, or a NaN or infinite scale, makes its row or column of Y NaN or infinite.
  * Rows past M are not read, and Y must not overlap what is read.  M == 0 is a no-op.  workspace:
  * hts_scaled_gemm_workspace() bytes (for any y_dtype), 16-byte aligned, or NULL: with less the product runs unsplit, with
